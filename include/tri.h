@@ -100,6 +100,17 @@ typedef enum {
     TRI_ENGINE_TENSOR = 2       /* tcgen05 scoring kernel, then the fused select and compaction */
 } tri_score_engine;
 
+/* How tri_rope_frequencies spreads the rotary frequencies for contexts longer than the original. */
+typedef enum {
+    TRI_ROPE_PLAIN = 0,   /* omega_f = base^(-2f/r) */
+    TRI_ROPE_LINEAR = 1,  /* omega_f / factor: positions interpolated */
+    TRI_ROPE_NTK = 2,     /* base factor^(r/(r-2)): the fastest band keeps its frequency, the slowest is divided by factor */
+    TRI_ROPE_YARN = 3,    /* omega_f / factor for bands that turn less than `low` times over the original length, omega_f
+                             for those that turn more than `high` times, a ramp over the bands between (their indices
+                             rounded outwards), and the magnitude 1 + 0.1 ln(factor) */
+    TRI_ROPE_SMOOTH = 4   /* the same ends, with a ramp over the number of turns between, and magnitude 1 */
+} tri_rope_scaling;
+
 /* Device-side problem codes reported by tri_get_error in *detail_code. */
 enum {
     TRI_DEV_NONE = 0,
@@ -107,7 +118,8 @@ enum {
     TRI_DEV_BAD_PAGE = 2,     /* a block-table entry outside [0, n_pages) */
     TRI_DEV_TIMEOUT = 3,      /* a bounded wait on an asynchronous copy gave up (unit-level) */
     TRI_DEV_INTERNAL = 4,     /* the selection did not produce exactly min(len, B) keys (unit-level) */
-    TRI_DEV_T_NOT_AFTER_POS = 5  /* a unit's last cached position is not below t (sequence-level) */
+    TRI_DEV_T_NOT_AFTER_POS = 5, /* a unit's last cached position is not below t (sequence-level) */
+    TRI_DEV_BAD_RANGE = 6     /* token ranges that do not ascend within the call's tokens (every sequence is refused) */
 };
 
 typedef struct tri_ctx tri_ctx;   /* opaque: device statistics, status word, counters */
@@ -297,6 +309,114 @@ TRI_API tri_status tri_prune_noalloc(tri_ctx *ctx, const tri_kv *kv, const int32
  * TRI_ECUDA.
  */
 TRI_API tri_status tri_decode_attention(tri_ctx *ctx, const tri_kv *kv, const void *q, float *out, void *stream);
+
+/*
+ * Rows of bf16 vectors that a call reads or writes: element (layer, token, head, dim) is at
+ * data[layer * layer_stride + token * token_stride + head * head_stride + dim]. Strides are in
+ * elements, multiples of 8 and not negative (0 repeats a row that is only read); data is device
+ * memory of the context's device, 16-byte aligned. The heads of one projection's output, or rows
+ * with the heads outermost, are such rows without a copy.
+ */
+typedef struct {
+    void *data;
+    int64_t layer_stride;
+    int64_t token_stride;
+    int64_t head_stride;
+} tri_rows;
+
+/*
+ * Rotary frequencies for tri_rope_load (host only; fp64). rotary_dim r: a multiple of 16 up to 128.
+ *   omega      [r/2], written: radians per position of each band
+ *   magnitude  written: what the rotated dims are multiplied by (1 but for TRI_ROPE_YARN)
+ * factor >= 1 (all but TRI_ROPE_PLAIN), original_length, low and high (TRI_ROPE_YARN, TRI_ROPE_SMOOTH;
+ * 0 < low < high) as tri_rope_scaling says. Errors: TRI_EINVAL.
+ */
+TRI_API tri_status tri_rope_frequencies(int rotary_dim, double base, int scaling, double factor,
+                                        double original_length, double low, double high, double *omega,
+                                        double *magnitude);
+
+/*
+ * The rotation that later tri_rope and tri_append_chunk calls apply: band f < r/2 of a row at position p is
+ * multiplied, as the complex number of its two dims, by magnitude e^{i omega_f p}. Dims at r and beyond stay.
+ *   rotary_dim r  a multiple of 16, up to 128 and, in each call, up to the head_dim
+ *   layout    TRI_ROPE_HALF: dims (f, f + r/2); TRI_ROPE_INTERLEAVED: dims (2f, 2f + 1)
+ *   omega     host fp64 [r/2], finite, copied; magnitude > 0
+ * Until this is called, the table is the loaded statistics' (base^(-2f/d) over the whole head, their layout).
+ * It replaces the table for tri_rope and tri_append_chunk only: the scores of tri_prune keep the frequencies of
+ * tri_calibrate_load. Synchronous (it waits for the device); a captured graph rotates by the table loaded
+ * when it is replayed, with the rotary_dim, layout and magnitude of its capture. Errors: TRI_EINVAL, TRI_ECUDA.
+ */
+TRI_API tri_status tri_rope_load(tri_ctx *ctx, int rotary_dim, int layout, const double *omega, double magnitude);
+
+/*
+ * Rotate rows (queries or keys) at their tokens' positions: out = rotation(x) for every layer, token and head.
+ *   x, out   tri_rows [n_layers][n_tokens][n_heads] of head_dim (64 or 128); out may be x itself (the same
+ *            data and strides), else they must not overlap; rows of out must not overlap one another
+ *   pos      int32 [n_tokens] device: any int32 position
+ *   inverse  0: rotate. Otherwise rotate back, divided by the magnitude: what post-RoPE rows were before
+ *            (pre-RoPE queries for tri_calibrate_estimate, from cached or logged ones)
+ * The angle is exact to about 2^-24 radians at every position, the products run in fp32, and the result is
+ * rounded to bf16 once. One launch on `stream`. n_tokens 0 is accepted. Errors: TRI_EINVAL, TRI_ESTATE (no table),
+ * TRI_EUNSUPPORTED, TRI_ECUDA.
+ */
+TRI_API tri_status tri_rope(tri_ctx *ctx, const tri_rows *x, const tri_rows *out, int n_layers, int n_tokens,
+                            int n_heads, int head_dim, const int32_t *pos, int inverse, void *stream);
+
+/*
+ * Append a run of new tokens to every sequence of a cache (dense or paged): the prompt's write, or several drafted
+ * tokens at once, with the keys rotated on the way.
+ *   kv        the cache; pos, lens and lens_out are required (lens_out may alias lens)
+ *   K_new, V_new  tri_rows [n_layers][n_tokens][n_kv_heads]: the new tokens of all sequences, one after another;
+ *             they must not overlap the cache
+ *   cu_new    int32 [batch + 1] device: sequence s has the tokens [cu_new[s], cu_new[s + 1]) (none, one or many).
+ *             Tokens outside every range are ignored
+ *   pos_new   int32 [n_tokens] device: each token's position
+ *   rotate    0: K_new is post-RoPE and copied. Otherwise keys are rotated at pos_new
+ *   q, q_out  both NULL, or (with rotate) tri_rows [n_layers][n_tokens][n_kv_heads * group]: the tokens' queries are
+ *             rotated in the same launch; q_out may be q itself, else they must not overlap
+ * Token i of sequence s goes to slot lens[s] + i of each of its units, and lens_out[s] = lens[s] + its tokens. Pages
+ * of those slots must be allocated; no page may be shared between the runs of two sequences. A sequence that
+ * would pass its capacity or lacks a page is refused as a whole: nothing of it is written (no row, no query,
+ * lens_out[s] = lens[s]) and tri_get_error reports TRI_DEV_LEN_GT_CAP or TRI_DEV_BAD_PAGE. Ranges that do not
+ * ascend within [0, n_tokens] refuse every sequence (TRI_DEV_BAD_RANGE). Rows and queries behind the last range
+ * are left as they were. One launch on `stream`, a programmatic dependent of the work before it as in tri_append.
+ * Needs the statistics loaded. The first call with more sequences than any before allocates 4 bytes per sequence
+ * (make it before a capture). Errors as tri_append, and TRI_ENOMEM.
+ */
+TRI_API tri_status tri_append_chunk(tri_ctx *ctx, const tri_kv *kv, const tri_rows *K_new, const tri_rows *V_new,
+                                    const int32_t *cu_new, const int32_t *pos_new, int n_tokens, int rotate,
+                                    const tri_rows *q, const tri_rows *q_out, void *stream);
+
+/*
+ * Attention of a chunk of new tokens over the cache (dense or paged) that already holds them: prompts, chunks of
+ * prompts, drafted tokens and single tokens, mixed as they come.
+ *   kv      the cache: K, V, lens (the new tokens included), block table and layer range are read
+ *   q       tri_rows [n_layers][n_tokens][n_kv_heads * group]: post-RoPE queries of the new tokens of all
+ *           sequences (strides above 0 in each dimension of more than one element)
+ *   cu_q    int32 [batch + 1] device: sequence s has the query tokens [cu_q[s], cu_q[s + 1]), its last n
+ *   scale   > 0: logits are scale q . k (1 / sqrt(head_dim) for the attention of tri_decode_attention)
+ *   causal  0: every query sees all lens[s] rows. Otherwise query i of n sees the rows [0, lens[s] - n + i + 1):
+ *           rows are ordered by slot, so after a prune too it sees all that is kept of what came before it
+ *   out     tri_rows like q, written: bf16
+ *   lse     fp32 [n_layers][n_tokens][n_kv_heads * group] device, written, or NULL: the natural logarithm of the sum of
+ *           exp(logit), with which attentions over other rows can be joined
+ * A query that sees no row (lens[s] of 0, or a query in front of the first row) gets zeros and an lse of -infinity. Rows
+ * at or past lens[s] and rows that a query does not see may hold anything, NaN included. Logits, softmax statistics and
+ * accumulators are fp32; the weights are rounded to bf16 for the tensor cores (2^-9 each), the result once more.
+ * Tokens outside every range are left unwritten; so are those of a refused sequence (TRI_DEV_LEN_GT_CAP,
+ * TRI_DEV_BAD_PAGE; TRI_DEV_BAD_RANGE refuses all). A wait that ran out (TRI_DEV_TIMEOUT) leaves the result of
+ * that call incomplete. Two launches on `stream` (a plan, and the attention as its programmatic dependent). The
+ * result does not depend on the order in which parts finish.
+ * Workspace of the context, allocated when a call needs more than any before (make the first call of the largest
+ * shape before a capture; later growth leaves what a captured graph uses in place): about 4 * SMs * 256 *
+ * (head_dim + 2) * 4 bytes (79 MB at head_dim 128), and 56 bytes per 256 query rows and sequence. The attention
+ * holds the whole tensor memory of every SM: do not run it beside other kernels that allocate tensor memory (see
+ * tri_set_offset_combine). Limits: n_layers * pages (or batch) * n_kv_heads * page size (or cap) below 2^31. Needs
+ * the statistics loaded. Errors: TRI_EINVAL, TRI_ESTATE, TRI_EUNSUPPORTED, TRI_ENOMEM, TRI_ECUDA.
+ */
+TRI_API tri_status tri_chunk_attention(tri_ctx *ctx, const tri_kv *kv, const tri_rows *q, const int32_t *cu_q,
+                                       int n_tokens, double scale, int causal, const tri_rows *out, float *lse,
+                                       void *stream);
 
 /*
  * Debug / parity entry: score without pruning.

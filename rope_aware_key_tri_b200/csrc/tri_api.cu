@@ -26,6 +26,8 @@
 #include "tri_append.cuh"
 #include "tri_maxdelta.cuh"
 #include "tri_attend.cuh"
+#include "tri_rope.cuh"
+#include "tri_chunk.cuh"
 
 struct tri_ctx {
     int device = -1;
@@ -57,6 +59,19 @@ struct tri_ctx {
     // chunk partials of tri_decode_attention, grown on demand
     float *d_att_part = nullptr;
     size_t att_part_bytes = 0;
+    // rotary table (tri_rope_load; the statistics' own frequencies until then)
+    double *d_turns = nullptr;
+    bool rope_loaded = false;
+    int rope_dim = 0, rope_layout = 0;
+    double rope_magnitude = 1.0;
+    // workspace of tri_append_chunk and tri_chunk_attention. A block that became too small stays
+    // allocated until the context goes, because a captured graph may still use it.
+    struct Block {
+        void *p = nullptr;
+        size_t bytes = 0;
+    } ws_new_len, ws_plan, ws_part;
+    std::vector<void *> ws_old;
+    unsigned *d_ticket = nullptr;
     // device bookkeeping
     unsigned long long *d_status = nullptr;
     // [0] CTAs of the fused kernel done, [1] its next free unit
@@ -208,6 +223,8 @@ struct Plan {
     int cs = 0, nslot = 0, kpc = 0, n_clusters = 0, extra = 0;
     size_t smem = 0;
 };
+
+constexpr int kMaxRopeDim = 128;
 
 // Capacity of the device list of units that a unit-level failure left uncompacted.
 constexpr int kFailCap = 4096;
@@ -1082,6 +1099,440 @@ tri_status run_attend(tri_ctx *c, const tri_kv *kv, const void *q, float *out, v
     return TRI_OK;
 }
 
+// ---------------------------------------------------------------------------------------
+// Rotary positions, runs of new tokens, and their attention.
+// ---------------------------------------------------------------------------------------
+
+// Memory of the context's own device (or managed): another device's would fault in the kernel.
+bool on_device(const tri_ctx *c, const void *p) {
+    if (!p) return false;
+    cudaPointerAttributes at;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == c->device);
+}
+
+// The context's device for the span of a call; the caller's own afterwards.
+struct DeviceGuard {
+    int before = -1;
+    cudaError_t error;
+    explicit DeviceGuard(int device) {
+        if (cudaGetDevice(&before) != cudaSuccess) before = -1;
+        error = cudaSetDevice(device);
+    }
+    ~DeviceGuard() {
+        if (before >= 0) cudaSetDevice(before);
+    }
+    DeviceGuard(const DeviceGuard &) = delete;
+    DeviceGuard &operator=(const DeviceGuard &) = delete;
+};
+
+// A workspace block of at least `need` bytes. The block it replaces is kept (see tri_ctx).
+tri_status ensure_block(tri_ctx *c, tri_ctx::Block *b, size_t need, const char *what) {
+    if (need <= b->bytes) return TRI_OK;
+    need = std::max(need, b->bytes + b->bytes / 2);  // so that the blocks kept stay a small multiple
+    void *p = nullptr;
+    const cudaError_t ce = cudaMalloc(&p, need);
+    if (ce != cudaSuccess) return cuda_fail(c, ce, what, TRI_ENOMEM);
+    if (b->p) {
+        try {
+            c->ws_old.push_back(b->p);
+        } catch (...) {
+            cudaFree(p);
+            return TRI_ENOMEM;
+        }
+    }
+    b->p = p;
+    b->bytes = need;
+    return TRI_OK;
+}
+
+// Rows [layers][tokens][heads][D] described by r: 16-byte aligned base and strides, device memory.
+// Written rows must not overlap: ordered by stride, each dimension steps over the one before.
+tri_status check_rows(tri_ctx *c, const tri_rows *r, long long layers, long long tokens, long long heads, int D,
+                      bool written, const char *what) {
+    const bool ok = r && r->data && aligned(r->data, 16) && on_device(c, r->data) && r->layer_stride % 8 == 0 &&
+                    r->token_stride % 8 == 0 && r->head_stride % 8 == 0 && r->layer_stride >= 0 &&
+                    r->token_stride >= 0 && r->head_stride >= 0;
+    if (!ok) {
+        std::snprintf(c->last_error, sizeof c->last_error,
+                      "%s: rows need device memory, a 16-byte aligned base and strides that are multiples of 8 elements", what);
+        return TRI_EINVAL;
+    }
+    if (written) {
+        struct Dim {
+            long long n, stride;
+        } d[3] = {{heads, r->head_stride}, {tokens, r->token_stride}, {layers, r->layer_stride}};
+        std::sort(d, d + 3, [](const Dim &x, const Dim &y) { return x.stride < y.stride; });
+        long long extent = D;
+        for (const Dim &x : d) {
+            if (x.n <= 1) continue;
+            if (x.stride < extent) {
+                std::snprintf(c->last_error, sizeof c->last_error, "%s: written rows overlap", what);
+                return TRI_EINVAL;
+            }
+            extent = x.stride * (x.n - 1) + extent;
+        }
+    }
+    return TRI_OK;
+}
+
+tri::RowSet row_set(const tri_rows *src, const tri_rows *dst, int heads) {
+    tri::RowSet s;
+    std::memset(&s, 0, sizeof s);
+    s.src = static_cast<const uint16_t *>(src->data);
+    s.src_l = src->layer_stride;
+    s.src_t = src->token_stride;
+    s.src_h = src->head_stride;
+    if (dst) {
+        s.dst = static_cast<uint16_t *>(dst->data);
+        s.dst_l = dst->layer_stride;
+        s.dst_t = dst->token_stride;
+        s.dst_h = dst->head_stride;
+    }
+    s.heads = heads;
+    return s;
+}
+
+template <int D, bool APPEND>
+const void *rope_kernel_of(int layout) {
+    return layout == 0 ? (const void *)&tri::tri_rope_kernel<D, 0, APPEND> : (const void *)&tri::tri_rope_kernel<D, 1, APPEND>;
+}
+
+// Tokens per CTA: enough units for every thread to have kRopeBatch of them, but no fewer CTAs than
+// eight a SM while there are that many tokens.
+tri_status launch_rope(tri_ctx *c, tri::RopeArgs &a, int D, int n_layers, bool append, void *stream) {
+    a.units = (a.q.heads + a.k.heads + a.v.heads) * (D / 16);
+    const long long want = (tri::kRopeThreads * tri::kRopeBatch + a.units - 1) / a.units;
+    const long long room = (long long)a.n_tokens * n_layers / (8LL * c->sm_count);
+    a.tpc = (int)std::max<long long>(1, std::min<long long>(tri::kRopeMaxTokens, std::min(want, room)));
+    a.units_magic = a.units > 1 ? (unsigned)(((1ull << 32) + a.units - 1) / a.units) : 0u;
+    const long long gx = std::max<long long>(1, ((long long)a.n_tokens + a.tpc - 1) / a.tpc);
+    if (gx > 0x7fffffffLL || n_layers > 65535 || gx * n_layers > 0x7fffffffLL) return TRI_EUNSUPPORTED;
+    const int layout = c->rope_layout;
+    const void *fn = D == 128 ? (append ? rope_kernel_of<128, true>(layout) : rope_kernel_of<128, false>(layout))
+                              : (append ? rope_kernel_of<64, true>(layout) : rope_kernel_of<64, false>(layout));
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3((unsigned)gx, (unsigned)n_layers);
+    cfg.blockDim = dim3((unsigned)tri::kRopeThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    void *params[] = {&a};
+    const cudaError_t ce = cudaLaunchKernelExC(&cfg, fn, params);
+    if (ce != cudaSuccess) return cuda_fail(c, ce, append ? "launch(append chunk)" : "launch(rope)");
+    return TRI_OK;
+}
+
+void rope_table(const tri_ctx *c, tri::RopeArgs *a, bool inverse) {
+    a->turns = c->d_turns;
+    a->rot = c->rope_dim;
+    a->mag_c = (float)(inverse ? 1.0 / c->rope_magnitude : c->rope_magnitude);
+    a->mag_s = (float)(inverse ? -1.0 / c->rope_magnitude : c->rope_magnitude);
+}
+
+tri_status run_rope(tri_ctx *c, const tri_rows *x, const tri_rows *out, int n_layers, int n_tokens, int n_heads,
+                    int head_dim, const int32_t *pos, int inverse, void *stream) {
+    if (!c || !x || !out) return TRI_EINVAL;
+    c->last_error[0] = 0;
+    if (!c->rope_loaded && !c->loaded) return TRI_ESTATE;
+    if (n_layers < 1 || n_tokens < 0 || n_heads < 1) return TRI_EINVAL;
+    if (head_dim != 64 && head_dim != 128) return TRI_EUNSUPPORTED;
+    if (c->rope_dim > head_dim) {
+        std::snprintf(c->last_error, sizeof c->last_error, "tri_rope: %d rotated dims in a head of %d", c->rope_dim, head_dim);
+        return TRI_EINVAL;
+    }
+    if (n_tokens == 0) return TRI_OK;
+    if (!pos || !on_device(c, pos) || !aligned(pos, 4)) return TRI_EINVAL;
+    if (n_heads > 65535) return TRI_EUNSUPPORTED;
+    tri_status st = check_rows(c, x, n_layers, n_tokens, n_heads, head_dim, false, "tri_rope: x");
+    if (st == TRI_OK) st = check_rows(c, out, n_layers, n_tokens, n_heads, head_dim, true, "tri_rope: out");
+    if (st != TRI_OK) return st;
+    const DeviceGuard guard(c->device);
+    if (guard.error != cudaSuccess) return cuda_fail(c, guard.error, "cudaSetDevice");
+    tri::RopeArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.q = row_set(x, out, n_heads);
+    a.pos = pos;
+    a.n_tokens = n_tokens;
+    rope_table(c, &a, inverse != 0);
+    return launch_rope(c, a, head_dim, n_layers, false, stream);
+}
+
+// The cache of a call that brings new tokens: shape, alignment, device memory; *cap_out the unit capacity.
+tri_status check_cache(tri_ctx *c, const tri_kv *kv, bool append, long long *cap_out) {
+    if (kv->batch < 1 || kv->n_layers < 1 || kv->layer_begin < 0 || kv->layer_begin + kv->n_layers > c->L)
+        return TRI_EINVAL;
+    const bool paged = kv->block_table != nullptr;
+    if (paged) {
+        if (kv->page_size < 16 || kv->page_size % 16 != 0 || kv->max_pages < 1 || kv->n_pages < 1) return TRI_EINVAL;
+        *cap_out = (long long)kv->page_size * kv->max_pages;
+    } else {
+        if (kv->cap < 1) return TRI_EINVAL;
+        *cap_out = kv->cap;
+    }
+    if (*cap_out > (1LL << 30)) return TRI_EUNSUPPORTED;
+    if (!kv->K || !kv->V || !kv->lens) return TRI_EINVAL;
+    if (!aligned(kv->K, 16) || !aligned(kv->V, 16) || !aligned(kv->lens, 4)) return TRI_EINVAL;
+    if (!on_device(c, kv->K) || !on_device(c, kv->V) || !on_device(c, kv->lens)) return TRI_EINVAL;
+    if (paged && (!on_device(c, kv->block_table) || !aligned(kv->block_table, 4))) return TRI_EINVAL;
+    if (append) {
+        if (!kv->pos || !kv->lens_out) return TRI_EINVAL;
+        if (!aligned(kv->pos, 4) || !on_device(c, kv->pos) || !aligned(kv->lens_out, 4) || !on_device(c, kv->lens_out))
+            return TRI_EINVAL;
+    }
+    if ((long long)kv->n_layers * kv->batch * c->Hkv > 0x7fffffffLL) return TRI_EUNSUPPORTED;
+    return TRI_OK;
+}
+
+tri_status run_append_chunk(tri_ctx *c, const tri_kv *kv, const tri_rows *K_new, const tri_rows *V_new,
+                            const int32_t *cu_new, const int32_t *pos_new, int n_tokens, int rotate, const tri_rows *q,
+                            const tri_rows *q_out, void *stream) {
+    if (!c || !kv || !cu_new) return TRI_EINVAL;
+    c->last_error[0] = 0;
+    if (!c->loaded) return TRI_ESTATE;
+    if (n_tokens < 0 || (q != nullptr) != (q_out != nullptr) || (q && !rotate)) return TRI_EINVAL;
+    long long cap_u = 0;
+    tri_status st = check_cache(c, kv, true, &cap_u);
+    if (st != TRI_OK) return st;
+    if (!on_device(c, cu_new) || !aligned(cu_new, 4)) return TRI_EINVAL;
+    const int D = c->D, Hkv = c->Hkv, Hq = Hkv * c->G, L = kv->n_layers;
+    if (rotate && c->rope_dim > D) {
+        std::snprintf(c->last_error, sizeof c->last_error, "tri_append_chunk: %d rotated dims in a head of %d", c->rope_dim, D);
+        return TRI_EINVAL;
+    }
+    if (Hq + 2 * Hkv > 65535) return TRI_EUNSUPPORTED;
+    tri::RopeArgs a;
+    std::memset(&a, 0, sizeof a);
+    if (n_tokens > 0) {
+        if (!pos_new || !on_device(c, pos_new) || !aligned(pos_new, 4)) return TRI_EINVAL;
+        if ((st = check_rows(c, K_new, L, n_tokens, Hkv, D, false, "tri_append_chunk: K_new")) != TRI_OK) return st;
+        if ((st = check_rows(c, V_new, L, n_tokens, Hkv, D, false, "tri_append_chunk: V_new")) != TRI_OK) return st;
+        if (q) {
+            if ((st = check_rows(c, q, L, n_tokens, Hq, D, false, "tri_append_chunk: q")) != TRI_OK) return st;
+            if ((st = check_rows(c, q_out, L, n_tokens, Hq, D, true, "tri_append_chunk: q_out")) != TRI_OK) return st;
+            a.q = row_set(q, q_out, Hq);
+        }
+        a.k = row_set(K_new, nullptr, Hkv);
+        a.v = row_set(V_new, nullptr, Hkv);
+    } else {
+        a.k.heads = a.v.heads = Hkv;
+    }
+    const DeviceGuard guard(c->device);
+    if (guard.error != cudaSuccess) return cuda_fail(c, guard.error, "cudaSetDevice");
+    if ((st = ensure_block(c, &c->ws_new_len, sizeof(int32_t) * (size_t)kv->batch, "cudaMalloc(new lengths)")) != TRI_OK)
+        return st;
+    a.pos = pos_new;
+    a.n_tokens = n_tokens;
+    if (rotate) {
+        rope_table(c, &a, false);
+    }
+    a.K = static_cast<uint16_t *>(kv->K);
+    a.V = static_cast<uint16_t *>(kv->V);
+    a.P = kv->pos;
+    a.cu = cu_new;
+    a.lens = kv->lens;
+    a.lens_out = kv->lens_out;
+    a.block_table = kv->block_table;
+    a.batch = kv->batch;
+    a.n_kv = Hkv;
+    a.page_size = kv->block_table ? kv->page_size : 0;
+    a.max_pages = kv->block_table ? kv->max_pages : 0;
+    a.n_pages = kv->block_table ? kv->n_pages : 0;
+    a.cap = kv->block_table ? 0 : kv->cap;
+    a.new_len = static_cast<int32_t *>(c->ws_new_len.p);
+    a.ticket = c->d_ticket;
+    a.status = c->d_status;
+    return launch_rope(c, a, D, L, true, stream);
+}
+
+// Tensor map of bf16 rows; dims and strides innermost first (strides in elements, from the second dim).
+bool encode_rows(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims,
+                 const long long *strides, const cuuint32_t *box) {
+    cuuint64_t gs[4];
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i + 1 < rank; ++i) gs[i] = (cuuint64_t)strides[i] * 2;
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), dims, gs, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, const int32_t *cu_q, int n_tokens,
+                               double scale, int causal, const tri_rows *out, float *lse, void *stream) {
+    if (!c || !kv || !cu_q) return TRI_EINVAL;
+    c->last_error[0] = 0;
+    if (!c->loaded) return TRI_ESTATE;
+    if (n_tokens < 0 || !(scale > 0.0) || !std::isfinite(scale)) return TRI_EINVAL;
+    long long cap_u = 0;
+    tri_status st = check_cache(c, kv, false, &cap_u);
+    if (st != TRI_OK) return st;
+    if (!on_device(c, cu_q) || !aligned(cu_q, 4)) return TRI_EINVAL;
+    const int D = c->D, G = c->G, Hkv = c->Hkv, Hq = Hkv * G, L = kv->n_layers;
+    if (n_tokens == 0) return TRI_OK;
+    if ((st = check_rows(c, q, L, n_tokens, Hq, D, false, "tri_chunk_attention: q")) != TRI_OK) return st;
+    if ((st = check_rows(c, out, L, n_tokens, Hq, D, true, "tri_chunk_attention: out")) != TRI_OK) return st;
+    if (lse && (!aligned(lse, 4) || !on_device(c, lse))) return TRI_EINVAL;
+    // a dimension of one element has no stride of its own; the others must step over at least a row
+    const long long dims[3] = {Hq, n_tokens, L};
+    long long strides[3] = {q->head_stride, q->token_stride, q->layer_stride};
+    for (int i = 0; i < 3; ++i) {
+        if (dims[i] == 1) strides[i] = D;
+        if (strides[i] < D) {
+            std::snprintf(c->last_error, sizeof c->last_error, "tri_chunk_attention: q: rows overlap");
+            return TRI_EINVAL;
+        }
+        if (strides[i] >= (1LL << 38)) return TRI_EUNSUPPORTED;
+    }
+    const bool paged = kv->block_table != nullptr;
+    const long long layer_rows = (paged ? (long long)kv->n_pages * kv->page_size : (long long)kv->batch * cap_u) * Hkv;
+    if (layer_rows * L >= (1LL << 31)) return TRI_EUNSUPPORTED;  // TMA row coordinates are int32
+    if (L > 65535 || Hkv > 8192) return TRI_EUNSUPPORTED;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) {
+        std::snprintf(c->last_error, sizeof c->last_error, "cuTensorMapEncodeTiled is not available");
+        return TRI_ECUDA;
+    }
+    const DeviceGuard guard(c->device);
+    if (guard.error != cudaSuccess) return cuda_fail(c, guard.error, "cudaSetDevice");
+    cudaError_t ce;
+
+    tri::ChunkArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.cu = cu_q;
+    a.lens = kv->lens;
+    a.block_table = kv->block_table;
+    a.n_tokens = n_tokens;
+    a.batch = kv->batch;
+    a.n_kv = Hkv;
+    a.n_layers = L;
+    a.group = G;
+    a.paged = paged ? 1 : 0;
+    a.page_size = paged ? kv->page_size : 0;
+    a.max_pages = paged ? kv->max_pages : 0;
+    a.n_pages = paged ? kv->n_pages : 0;
+    a.cap_u = (int)cap_u;
+    a.causal = causal ? 1 : 0;
+    // the largest box that no page boundary cuts
+    a.piece_rows = !paged || kv->page_size % 128 == 0 ? 128 : kv->page_size % 64 == 0 ? 64 : kv->page_size % 32 == 0 ? 32 : 16;
+    a.sm_count = c->sm_count;
+    a.c = (float)(scale * 1.4426950408889634);
+    a.q = static_cast<const uint16_t *>(q->data);
+    a.q_l = q->layer_stride;
+    a.q_t = q->token_stride;
+    a.q_h = q->head_stride;
+    a.out = static_cast<uint16_t *>(out->data);
+    a.o_l = out->layer_stride;
+    a.o_t = out->token_stride;
+    a.o_h = out->head_stride;
+    a.lse = lse;
+    a.K = static_cast<const uint16_t *>(kv->K);
+    a.V = static_cast<const uint16_t *>(kv->V);
+    a.status = c->d_status;
+    a.wait_tries = c->wait_tries;
+    a.inject_unit = c->inject_unit;
+
+    // workspace: blocks are at most one per sequence more than the full ones; partial results are
+    // bounded by the plan, which takes no split that needs more slots
+    a.max_slots = 4 * c->sm_count;
+    const long long blocks = (long long)n_tokens * G / tri::kChunkRows + kv->batch;
+    const long long entries = blocks + a.max_slots;
+    if (entries * L * Hkv > (1LL << 40) || entries > (1LL << 30)) return TRI_EUNSUPPORTED;
+    a.max_entries = (int)entries;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    const size_t o_head = take(sizeof(tri::ChunkHead)), o_seqs = take(sizeof(tri::ChunkSeq) * (size_t)kv->batch),
+                 o_base = take(sizeof(int) * ((size_t)kv->batch + 1)), o_tiles = take(sizeof(int) * (size_t)blocks),
+                 o_per = take(sizeof(int) * (size_t)blocks), o_counters = take(sizeof(unsigned) * 2 * (size_t)a.max_slots),
+                 o_entries = take(sizeof(tri::ChunkEntry) * (size_t)entries);
+    const size_t part_floats = (size_t)a.max_slots * 2 * 128 * D, ml_floats = (size_t)a.max_slots * 2 * 128 * 2;
+    const bool fresh = off > c->ws_plan.bytes;
+    if ((st = ensure_block(c, &c->ws_plan, off, "cudaMalloc(attention plan)")) != TRI_OK) return st;
+    if ((st = ensure_block(c, &c->ws_part, (part_floats + ml_floats) * sizeof(float), "cudaMalloc(attention parts)")) != TRI_OK)
+        return st;
+    unsigned char *ws = static_cast<unsigned char *>(c->ws_plan.p);
+    a.head = reinterpret_cast<tri::ChunkHead *>(ws + o_head);
+    a.seqs = reinterpret_cast<tri::ChunkSeq *>(ws + o_seqs);
+    a.base = reinterpret_cast<int *>(ws + o_base);
+    a.tiles = reinterpret_cast<int *>(ws + o_tiles);
+    a.per = reinterpret_cast<int *>(ws + o_per);
+    a.counters = reinterpret_cast<unsigned *>(ws + o_counters);
+    a.entries = reinterpret_cast<tri::ChunkEntry *>(ws + o_entries);
+    a.part = static_cast<float *>(c->ws_part.p);
+    a.part_ml = a.part + part_floats;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (fresh) {
+        ce = cudaMemsetAsync(a.head, 0, sizeof(tri::ChunkHead), cs);  // the ticket; every plan leaves it at zero
+        if (ce != cudaSuccess) return cuda_fail(c, ce, "cudaMemsetAsync(plan)");
+    }
+
+    CUtensorMap qmap, kmap, vmap;
+    const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)n_tokens, (cuuint64_t)L};
+    const cuuint32_t qbox[4] = {64u, (cuuint32_t)G, (cuuint32_t)(128 / G), 1u};
+    const cuuint64_t kd[2] = {(cuuint64_t)D, (cuuint64_t)(layer_rows * L)};
+    const long long ks[1] = {D};
+    const cuuint32_t kbox[2] = {64u, (cuuint32_t)a.piece_rows};
+    if (!encode_rows(encode, &qmap, a.q, 4, qd, strides, qbox) || !encode_rows(encode, &kmap, a.K, 2, kd, ks, kbox) ||
+        !encode_rows(encode, &vmap, a.V, 2, kd, ks, kbox)) {
+        std::snprintf(c->last_error, sizeof c->last_error, "cuTensorMapEncodeTiled failed");
+        return TRI_ECUDA;
+    }
+    // ring: as many stages as fit beside the query tiles, which also keeps it to one CTA per SM (each
+    // allocates the whole tensor memory)
+    a.nst = D == 128 ? 5 : 8;
+    const unsigned smem = tri::chunk_smem(D, a.nst).total;
+    const void *fn = D == 128 ? (const void *)&tri::tri_chunk_kernel<128> : (const void *)&tri::tri_chunk_kernel<64>;
+    ce = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (ce != cudaSuccess) return cuda_fail(c, ce, "cudaFuncSetAttribute(chunk)");
+
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3((unsigned)kv->batch);
+    cfg.blockDim = dim3((unsigned)tri::kChunkPlanThreads);
+    cfg.stream = cs;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    ce = cudaLaunchKernelEx(&cfg, tri::tri_chunk_plan_kernel, a);
+    if (ce != cudaSuccess) return cuda_fail(c, ce, "launch(chunk plan)");
+    cfg.gridDim = dim3((unsigned)std::min<long long>(c->sm_count, entries * L * Hkv));
+    cfg.blockDim = dim3((unsigned)tri::kChunkThreads);
+    cfg.dynamicSmemBytes = smem;
+    void *params[] = {&qmap, &kmap, &vmap, &a};
+    ce = cudaLaunchKernelExC(&cfg, fn, params);
+    if (ce != cudaSuccess) return cuda_fail(c, ce, "launch(chunk attention)");
+    return TRI_OK;
+}
+
+// Turns per position of the bands, to the device (replaces the table before).
+tri_status set_rope_table(tri_ctx *c, const double *omega, int rotary_dim, int layout, double magnitude) {
+    std::vector<double> turns((size_t)rotary_dim / 2);
+    for (size_t f = 0; f < turns.size(); ++f) turns[f] = omega[f] / 6.283185307179586476925;
+    const DeviceGuard guard(c->device);
+    if (guard.error != cudaSuccess) return cuda_fail(c, guard.error, "cudaSetDevice");
+    cudaError_t ce;
+    // the synchronous copy follows work already launched on blocking streams; a table is otherwise
+    // replaced only when no call uses it
+    if ((ce = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(c, ce, "cudaDeviceSynchronize");
+    ce = cudaMemcpy(c->d_turns, turns.data(), sizeof(double) * turns.size(), cudaMemcpyHostToDevice);
+    if (ce != cudaSuccess) return cuda_fail(c, ce, "cudaMemcpy(rotary table)");
+    c->rope_dim = rotary_dim;
+    c->rope_layout = layout;
+    c->rope_magnitude = magnitude;
+    return TRI_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1106,6 +1557,8 @@ tri_status tri_create(tri_ctx **out, int device) {
     c->max_smem_optin = (int)p.sharedMemPerBlockOptin;
     if (cudaMalloc(&c->d_status, sizeof(unsigned long long)) != cudaSuccess ||
         cudaMalloc(&c->d_counter, 2 * sizeof(unsigned int)) != cudaSuccess ||
+        cudaMalloc(&c->d_turns, sizeof(double) * kMaxRopeDim / 2) != cudaSuccess ||
+        cudaMalloc(&c->d_ticket, sizeof(unsigned)) != cudaSuccess ||
         cudaMalloc(&c->d_fail_count, sizeof(unsigned)) != cudaSuccess ||
         cudaMalloc(&c->d_fail_units, sizeof(int32_t) * kFailCap) != cudaSuccess) {
         tri_destroy(c);
@@ -1113,6 +1566,7 @@ tri_status tri_create(tri_ctx **out, int device) {
     }
     if (cudaMemset(c->d_status, 0, sizeof(unsigned long long)) != cudaSuccess ||
         cudaMemset(c->d_counter, 0, 2 * sizeof(unsigned int)) != cudaSuccess ||
+        cudaMemset(c->d_ticket, 0, sizeof(unsigned)) != cudaSuccess ||
         cudaMemset(c->d_fail_count, 0, sizeof(unsigned)) != cudaSuccess) {
         tri_destroy(c);
         return TRI_ECUDA;
@@ -1137,6 +1591,12 @@ tri_status tri_destroy(tri_ctx *c) {
     cudaFree(c->d_tile_prefix);
     cudaFree(c->d_unit_fail);
     cudaFree(c->d_att_part);
+    cudaFree(c->d_turns);
+    cudaFree(c->d_ticket);
+    cudaFree(c->ws_new_len.p);
+    cudaFree(c->ws_plan.p);
+    cudaFree(c->ws_part.p);
+    for (void *p : c->ws_old) cudaFree(p);
     delete c;
     return TRI_OK;
 }
@@ -1210,7 +1670,78 @@ tri_status tri_calibrate_load(tri_ctx *c, int n_layers, int n_kv_heads, int grou
     c->D = D;
     c->layout = layout;
     c->loaded = true;
+    // until tri_rope_load, tokens are rotated at the statistics' own frequencies
+    if (!c->rope_loaded) return set_rope_table(c, omega.data(), D, layout, 1.0);
     return TRI_OK;
+}
+
+tri_status tri_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double original_length,
+                                double low, double high, double *omega, double *magnitude) {
+    if (!omega || !magnitude || rotary_dim < 16 || rotary_dim % 16 != 0 || rotary_dim > kMaxRopeDim) return TRI_EINVAL;
+    if (!(base > 1.0) || !std::isfinite(base)) return TRI_EINVAL;
+    const bool scaled = scaling != TRI_ROPE_PLAIN, by_band = scaling == TRI_ROPE_YARN || scaling == TRI_ROPE_SMOOTH;
+    if (scaling < TRI_ROPE_PLAIN || scaling > TRI_ROPE_SMOOTH) return TRI_EINVAL;
+    if (scaled && (!(factor >= 1.0) || !std::isfinite(factor))) return TRI_EINVAL;
+    if (by_band && (!(original_length > 0.0) || !std::isfinite(original_length) || !(low > 0.0) || !(high > low) ||
+                    !std::isfinite(high)))
+        return TRI_EINVAL;
+    const double two_pi = 6.283185307179586476925, r = rotary_dim;
+    const int F = rotary_dim / 2;
+    double b = base, mag = 1.0;
+    if (scaling == TRI_ROPE_NTK) b = base * std::pow(factor, r / (r - 2.0));
+    for (int f = 0; f < F; ++f) omega[f] = std::pow(b, -2.0 * f / r);
+    if (scaling == TRI_ROPE_LINEAR)
+        for (int f = 0; f < F; ++f) omega[f] /= factor;
+    if (scaling == TRI_ROPE_YARN) {
+        // the band that turns x times over the original length, as a real number
+        auto band = [&](double x) { return r * std::log(original_length / (x * two_pi)) / (2.0 * std::log(base)); };
+        const double lo = std::max(std::floor(band(high)), 0.0), hi = std::min(std::ceil(band(low)), r - 1.0);
+        for (int f = 0; f < F; ++f) {
+            const double ramp = std::min(1.0, std::max(0.0, (f - lo) / std::max(hi - lo, 1e-3)));
+            omega[f] = omega[f] * (1.0 - ramp) + omega[f] / factor * ramp;
+        }
+        mag = 0.1 * std::log(factor) + 1.0;
+    }
+    if (scaling == TRI_ROPE_SMOOTH)
+        for (int f = 0; f < F; ++f) {
+            const double turns = original_length * omega[f] / two_pi;
+            const double mix = std::min(1.0, std::max(0.0, (turns - low) / (high - low)));
+            omega[f] = omega[f] / factor * (1.0 - mix) + omega[f] * mix;
+        }
+    *magnitude = mag;
+    return TRI_OK;
+}
+
+tri_status tri_rope_load(tri_ctx *c, int rotary_dim, int layout, const double *omega, double magnitude) {
+    if (!c || !omega) return TRI_EINVAL;
+    c->last_error[0] = 0;
+    if (rotary_dim < 16 || rotary_dim % 16 != 0 || rotary_dim > kMaxRopeDim) return TRI_EINVAL;
+    if (layout != TRI_ROPE_HALF && layout != TRI_ROPE_INTERLEAVED) return TRI_EINVAL;
+    if (!(magnitude > 0.0) || !std::isfinite(magnitude)) return TRI_EINVAL;
+    for (int f = 0; f < rotary_dim / 2; ++f)
+        if (!std::isfinite(omega[f])) return TRI_EINVAL;
+    const tri_status st = set_rope_table(c, omega, rotary_dim, layout, magnitude);
+    if (st == TRI_OK) c->rope_loaded = true;
+    return st;
+}
+
+tri_status tri_rope(tri_ctx *c, const tri_rows *x, const tri_rows *out, int n_layers, int n_tokens, int n_heads,
+                    int head_dim, const int32_t *pos, int inverse, void *stream) {
+    NvtxRange r("tri_rope");
+    return run_rope(c, x, out, n_layers, n_tokens, n_heads, head_dim, pos, inverse, stream);
+}
+
+tri_status tri_append_chunk(tri_ctx *c, const tri_kv *kv, const tri_rows *K_new, const tri_rows *V_new,
+                            const int32_t *cu_new, const int32_t *pos_new, int n_tokens, int rotate, const tri_rows *q,
+                            const tri_rows *q_out, void *stream) {
+    NvtxRange r("tri_append_chunk");
+    return run_append_chunk(c, kv, K_new, V_new, cu_new, pos_new, n_tokens, rotate, q, q_out, stream);
+}
+
+tri_status tri_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, const int32_t *cu_q, int n_tokens,
+                               double scale, int causal, const tri_rows *out, float *lse, void *stream) {
+    NvtxRange r("tri_chunk_attention");
+    return run_chunk_attention(c, kv, q, cu_q, n_tokens, scale, causal, out, lse, stream);
 }
 
 tri_status tri_prune(tri_ctx *c, const tri_kv *kv, const int32_t *t, int32_t budget, void *stream) {

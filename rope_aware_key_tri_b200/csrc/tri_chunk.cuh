@@ -1,0 +1,964 @@
+// tri_chunk.cuh -- attention of a chunk of new tokens over the cache, for sm_100a.
+//
+// Sequence s brings n tokens (their rows already in the cache as its last n of len). For query head
+// h of new token i, with the KV head g = h / G of its group,
+//   out = sum_j softmax_j(scale q . k_j) v_j,  j < len - n + i + 1 (causal) or j < len,
+//   lse = log sum_j exp(scale q . k_j),
+// zeros and -inf where no key is left. The running maximum m and sum l of a row turn this into one
+// pass over the keys: with p_j = 2^((x_j - m) c), c = scale log2(e), out = sum p_j v_j / sum p_j.
+//
+// Two launches. The plan kernel (one CTA per sequence) checks the sequence (range of tokens, length,
+// pages); its last CTA lists the work, so that nothing waits on the host. An item is a block of
+// kChunkRows rows of a KV head's packed query matrix (row = token * G + head in group, so that all G
+// query heads of a key share its one read), over a range of 128-key tiles. Where there are too few
+// items to fill the SMs evenly, items are split over the keys; the last CTA of an item to finish
+// merges the partial results in the order of the keys, so the result does not depend on which it is.
+// Items are handed out longest first, in rounds that run forth and back over the CTAs.
+//
+// The attention kernel, one persistent CTA per SM: warp 0 loads (TMA, 128-byte swizzle: the item's
+// query rows, then K and V tiles through a ring), warp 1 issues the tcgen05 MMAs, and two warpgroups
+// take one 128-row query tile each, a row per thread:
+//   S_q = Q_q K^T            128 x 128 x D into TMEM columns [128 q, 128 q + 128)
+//   P_q = 2^((S_q - m) c)    read, masked, exponentiated, rounded to bf16 and written over S_q
+//   O_q += P_q V             A from TMEM, V as the N-major operand: the tile lies as it came
+// The MMA warp runs O_q += P_q V(i) and S_q = Q_q K(i+1)^T back to back, so that one warpgroup's
+// exponentials overlap the other's MMAs; S_q(i+1) complete implies P_q V(i) complete, so O_q is the
+// warpgroup's own until it hands over P_q(i+1): it rescales O_q itself, and only where the maximum
+// has grown by more than 2^8 since the last rescale (p then stays below 2^8; nothing is lost, the
+// quotient is the same).
+//
+// Precision: logits, m, l and O are fp32. P is rounded to bf16 (the MMA's A has V's type): each
+// weight moves by at most 2^-9 relative, independent from key to key, which adds about as much to the
+// result as its own final rounding to bf16. l sums the unrounded weights.
+//
+// Bound: a 256 x 128 pair of tiles is 4 * 256 * 128 * D flops on the tensor cores against 256 * 128
+// exponentials at 16 a clock and SM (D = 128: 2048 clocks each); below about 60 rows per key the HBM.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "tri_kernel.cuh"
+#include "tri_maxdelta.cuh"
+#include "tri_rope.cuh"
+
+namespace tri {
+
+constexpr int kChunkRows = 256;     // packed query rows of an item: two MMA tiles
+constexpr int kChunkThreads = 384;  // a warpgroup with the load and the MMA warp, two for the softmax
+// Registers a thread after the split: 128 * 72 + 256 * 216 = 64512, the 384 * 168 that the
+// block is launched with. A softmax thread holds a row of 128 logits.
+constexpr int kChunkRegsFew = 72, kChunkRegsMany = 216;
+constexpr int kChunkPlanThreads = 256;
+constexpr int kChunkMaxStages = 8;
+
+// One line of the plan: a block of rows of one sequence over the key tiles [kt0, kt1), for every
+// layer and KV head.
+struct __align__(16) ChunkEntry {
+    int s, tok0, ntok, len;   // sequence, first token (global row), tokens of the block, cached rows
+    int first, kt0, kt1;      // keys seen by the block's first row, key tiles
+    int nsplit, split, slot, group, pad;  // splits of the block; this one; its first partial; its counter
+};
+
+struct ChunkSeq {
+    int q0, n, len, bad;
+};
+
+struct ChunkHead {
+    int n_entries;            // lines of the plan
+    unsigned ticket;          // plan CTAs done (back to 0 at the end)
+};
+
+struct ChunkArgs {
+    const int32_t *cu;        // [batch + 1]
+    const int32_t *lens;
+    const int32_t *block_table;
+    int n_tokens, batch, n_kv, n_layers, group;
+    int paged, page_size, max_pages, n_pages, cap_u;
+    int causal;
+    int piece_rows;           // rows of a key box
+    int nst;                  // ring stages
+    int sm_count, max_slots, max_entries;
+    float c;                  // scale * log2(e)
+    // where the query rows and results are (strides in elements)
+    const uint16_t *q;
+    long long q_l, q_t, q_h;
+    uint16_t *out;
+    long long o_l, o_t, o_h;
+    float *lse;               // [n_layers][n_tokens][Hq] or null
+    const uint16_t *K, *V;
+    // workspace
+    ChunkHead *head;
+    ChunkSeq *seqs;           // [batch]
+    int *base;                // [batch + 1] blocks before each sequence
+    int *tiles;               // [max blocks] key tiles of each block
+    int *per;                 // (scratch of the plan) tiles of a split of each block
+    ChunkEntry *entries;
+    float *part;              // [slot][tile][D / 4][128][4], then [slot][tile][128][2] (m, l)
+    float *part_ml;
+    unsigned *counters;       // [group][tile]
+    unsigned long long *status;
+    int wait_tries;
+    long long inject_unit;
+};
+
+__host__ __device__ inline int chunk_blocks(int n, int G) { return (n + kChunkRows / G - 1) / (kChunkRows / G); }
+
+// ---------------------------------------------------------------------------------
+// The plan.
+// ---------------------------------------------------------------------------------
+// Costs in units of one key tile of an item: what a further item costs its CTA (filling and draining
+// the pipeline, the result), and what the merge of a split adds at the end.
+constexpr int kChunkItemCost = 2;
+constexpr int kChunkMergeCost = 2;
+constexpr int kChunkSortBins = 1024;
+
+__global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const ChunkArgs a) {
+    constexpr unsigned FULL = 0xffffffffu;
+    __shared__ int sh_bad, sh_last, sh_scan[kChunkPlanThreads / 32], sh_run;
+    __shared__ int hist[kChunkSortBins];
+    __shared__ long long est[8];
+    __shared__ int est_chunk[8];
+    __shared__ long long sh_sum;
+    __shared__ int sh_max, sh_entries, sh_slots, sh_groups, sh_chunk;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int s0 = blockIdx.x;
+    {
+        const int lo = __ldg(a.cu + s0), hi = __ldg(a.cu + s0 + 1), len = __ldg(a.lens + s0);
+        const long long cap = a.cap_u;
+        int bad = 0;
+        if (lo < 0 || lo > hi || hi > a.n_tokens) bad = kDevBadRange;
+        else if (len < 0 || len > cap) bad = 1;  // TRI_DEV_LEN_GT_CAP
+        if (tid == 0) sh_bad = 0;
+        __syncthreads();
+        if (!bad && a.paged && hi > lo) {
+            const int np = (len + a.page_size - 1) / a.page_size;
+            bool ok = true;
+            for (int p = tid; p < np; p += kChunkPlanThreads) {
+                const int id = __ldg(a.block_table + (long long)s0 * a.max_pages + p);
+                ok = ok && id >= 0 && id < a.n_pages;
+            }
+            if (!ok) sh_bad = 2;                 // TRI_DEV_BAD_PAGE
+        }
+        __syncthreads();
+        if (!bad) bad = sh_bad;
+        if (tid == 0) {
+            a.seqs[s0] = ChunkSeq{lo, hi - lo, len, bad};
+            if (bad) record_status(a.status, bad, (long long)s0 * a.n_kv);
+            __threadfence();
+            sh_last = atomicAdd(&a.head->ticket, 1u) == gridDim.x - 1;
+        }
+    }
+    __syncthreads();
+    if (!sh_last) return;
+    __threadfence();
+
+    // blocks before each sequence; a bad range refuses every sequence (the ranges may overlap)
+    bool range_ok = true;
+    for (int s = tid; s < a.batch; s += kChunkPlanThreads) range_ok = range_ok && __ldcg(&a.seqs[s].bad) != kDevBadRange;
+    range_ok = __syncthreads_and(range_ok);
+    if (tid == 0) {
+        sh_run = 0;
+        sh_sum = 0;
+        sh_max = 0;
+        a.head->ticket = 0;
+    }
+    __syncthreads();
+    const int G = a.group, tpb = kChunkRows / G;
+    for (int c0 = 0; c0 < a.batch; c0 += kChunkPlanThreads) {
+        const int s = c0 + tid;
+        int nb = 0;
+        if (range_ok && s < a.batch && __ldcg(&a.seqs[s].bad) == 0) nb = chunk_blocks(__ldcg(&a.seqs[s].n), G);
+        int inc = nb;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(FULL, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) sh_scan[warp] = inc;
+        __syncthreads();
+        int before = sh_run;
+        for (int w = 0; w < warp; ++w) before += sh_scan[w];
+        if (s < a.batch) a.base[s] = before + inc - nb;
+        __syncthreads();
+        if (tid == kChunkPlanThreads - 1) sh_run = before + inc;
+        __syncthreads();
+    }
+    const int n_blocks = sh_run;
+    if (tid == 0) a.base[a.batch] = n_blocks;
+    __syncthreads();
+    const int LH = a.n_layers * a.n_kv;
+    // sequence of block e, and its line without splits
+    auto block_of = [&](int e) {
+        int lo = 0, hi = a.batch;  // the last s with base[s] <= e: empty sequences before it are skipped
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.base[mid] <= e) lo = mid; else hi = mid;
+        }
+        const int n = __ldcg(&a.seqs[lo].n), len = __ldcg(&a.seqs[lo].len);
+        const int b = e - a.base[lo];
+        ChunkEntry x;
+        x.s = lo;
+        x.tok0 = __ldcg(&a.seqs[lo].q0) + b * tpb;
+        x.ntok = min(tpb, n - b * tpb);
+        x.len = len;
+        x.first = a.causal ? len - n + b * tpb + 1 : len;
+        const int end = a.causal ? min(len, max(0, x.first + x.ntok - 1)) : len;
+        x.kt0 = 0;
+        x.kt1 = (end + 127) / 128;
+        x.nsplit = 1;
+        x.split = 0;
+        x.slot = 0;
+        x.group = 0;
+        x.pad = 0;
+        return x;
+    };
+    {
+        long long sum = 0;
+        int mx = 0;
+        for (int e = tid; e < n_blocks; e += kChunkPlanThreads) {
+            const ChunkEntry x = block_of(e);
+            a.tiles[e] = x.kt1;
+            sum += x.kt1;
+            mx = max(mx, x.kt1);
+        }
+        for (int o = 16; o; o >>= 1) {
+            sum += __shfl_xor_sync(FULL, sum, o);
+            mx = max(mx, __shfl_xor_sync(FULL, mx, o));
+        }
+        if (lane == 0) {
+            atomicAdd(reinterpret_cast<unsigned long long *>(&sh_sum), (unsigned long long)sum);
+            atomicMax(&sh_max, mx);
+        }
+    }
+    __syncthreads();
+    // the longest split: warp w weighs one candidate, a share of an SM's even part of the work. The
+    // time of a candidate is at most rounds * longest and at most even part + longest (both bounds
+    // of handing items out longest first); the smaller of them counts.
+    {
+        const long long even = (sh_sum * LH + a.sm_count - 1) / a.sm_count;
+        // even, 2/3, 1/2, 2/5, 1/3, 1/4, 1/6 of it; warp 0 does not split
+        const int num[8] = {1, 1, 2, 1, 2, 1, 1, 1}, den[8] = {1, 1, 3, 2, 5, 3, 4, 6};
+        const long long want = (even * num[warp] + den[warp] - 1) / den[warp];
+        const int chunk = warp == 0 ? max(1, sh_max) : (int)max(2LL, min((long long)max(1, sh_max), want));
+        long long items = 0, work = 0;
+        int longest = 0, slots = 0, lines = 0;
+        for (int e = lane; e < n_blocks; e += 32) {
+            const int t = a.tiles[e];
+            int ns = max(1, (t + chunk - 1) / chunk);
+            const int per = (t + ns - 1) / ns;
+            if (t > 0) ns = (t + per - 1) / per;
+            items += ns;
+            lines += ns;
+            work += t + (long long)ns * kChunkItemCost;
+            longest = max(longest, per);
+            if (ns > 1) slots += ns;
+        }
+        for (int o = 16; o; o >>= 1) {
+            items += __shfl_xor_sync(FULL, items, o);
+            work += __shfl_xor_sync(FULL, work, o);
+            longest = max(longest, __shfl_xor_sync(FULL, longest, o));
+            slots += __shfl_xor_sync(FULL, slots, o);
+            lines += __shfl_xor_sync(FULL, lines, o);
+        }
+        if (lane == 0) {
+            const long long rounds = (items * LH + a.sm_count - 1) / a.sm_count;
+            const long long one = longest + kChunkItemCost;
+            long long cost = min(rounds * one, (work * LH + a.sm_count - 1) / a.sm_count + one);
+            if (slots > 0) cost += kChunkMergeCost;
+            if ((long long)slots * LH > a.max_slots || lines > a.max_entries) cost = 1LL << 60;
+            est[warp] = cost;
+            est_chunk[warp] = chunk;
+        }
+    }
+    for (int i = tid; i < kChunkSortBins; i += kChunkPlanThreads) hist[i] = 0;
+    __syncthreads();
+    if (tid == 0) {
+        int best = 0;
+        for (int w = 1; w < 8; ++w)
+            if (est[w] < est[best]) best = w;
+        sh_chunk = est_chunk[best];
+        sh_slots = 0;
+        sh_groups = 0;
+    }
+    __syncthreads();
+    // lines of each length, longest first
+    const int chunk = sh_chunk;
+    auto bin_of = [](int per) { return kChunkSortBins - 1 - min(per, kChunkSortBins - 1); };
+    for (int e = tid; e < n_blocks; e += kChunkPlanThreads) {
+        const int t = a.tiles[e];
+        int ns = max(1, (t + chunk - 1) / chunk);
+        const int per = (t + ns - 1) / ns;
+        if (t > 0) ns = (t + per - 1) / per;
+        a.per[e] = per;
+        atomicAdd(&hist[bin_of(per)], ns);
+    }
+    __syncthreads();
+    if (warp == 0) {  // exclusive prefix sums of the bins
+        int run = 0;
+        for (int i0 = 0; i0 < kChunkSortBins; i0 += 32) {
+            const int x = hist[i0 + lane];
+            int inc = x;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(FULL, inc, o);
+                if (lane >= o) inc += y;
+            }
+            hist[i0 + lane] = run + inc - x;
+            run += __shfl_sync(FULL, inc, 31);
+        }
+        if (lane == 0) sh_entries = run;
+    }
+    __syncthreads();
+    for (int e = tid; e < n_blocks; e += kChunkPlanThreads) {
+        ChunkEntry x = block_of(e);
+        const int t = x.kt1, per = a.per[e];
+        const int ns = t > 0 ? (t + per - 1) / per : 1;
+        const int at = atomicAdd(&hist[bin_of(per)], ns);
+        x.nsplit = ns;
+        if (ns > 1) {
+            x.slot = atomicAdd(&sh_slots, ns);
+            x.group = atomicAdd(&sh_groups, 1);
+        }
+        for (int k = 0; k < ns; ++k) {
+            x.split = k;
+            x.kt0 = k * per;
+            x.kt1 = min(t, (k + 1) * per);
+            a.entries[at + k] = x;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < 2 * sh_groups * LH; i += kChunkPlanThreads) a.counters[i] = 0;
+    if (tid == 0) a.head->n_entries = sh_entries;
+}
+
+// ---------------------------------------------------------------------------------
+// PTX of the attention kernel.
+// ---------------------------------------------------------------------------------
+__device__ __forceinline__ void tma_tile_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_tile_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+// Shared-memory matrix descriptors in the 128-byte swizzle as (low, high) words: the start address and
+// the leading offset, in units of 16 bytes, are the low word, to which a k-step adds a constant. The
+// high word: 8-row groups 1024 bytes apart, descriptor version 1, swizzle mode.
+constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t smem_addr, unsigned lead_bytes) {
+    return (smem_addr >> 4) | ((lead_bytes >> 4) << 16);
+}
+__device__ __forceinline__ void chunk_mma_ss(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, int acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_low), "r"(b_low), "r"(idesc), "r"(acc), "r"(kDescHigh)
+        : "memory");
+}
+// A (bf16 pairs, one row per lane) in tensor memory.
+__device__ __forceinline__ void chunk_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, int acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(acc), "r"(kDescHigh)
+        : "memory");
+}
+
+#define TRI_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define TRI_U8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+#define TRI_W8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+
+// 32 columns of this warp's 32 TMEM lanes; valid after tmem_wait32 on the same registers.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : TRI_R8(r, 0), TRI_R8(r, 8), TRI_R8(r, 16), TRI_R8(r, 24)
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::TRI_U8(r, 0),
+        TRI_U8(r, 8), TRI_U8(r, 16), TRI_U8(r, 24), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : TRI_W8(r, 0), TRI_W8(r, 8), TRI_W8(r, 16), TRI_W8(r, 24) : : "memory");
+}
+// Orders later uses of r after a tmem_wait32 issued just before (no instruction).
+__device__ __forceinline__ void tmem_after32(uint32_t (&r)[32]) {
+    asm volatile("" : TRI_W8(r, 0), TRI_W8(r, 8), TRI_W8(r, 16), TRI_W8(r, 24) : : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+struct ChunkSmem {
+    unsigned q, ring, bars, total;
+};
+__host__ __device__ inline ChunkSmem chunk_smem(int D, int nst) {
+    ChunkSmem L;
+    L.q = 0;
+    L.ring = 2u * (unsigned)D * 256u;               // two query tiles of 128 rows
+    L.bars = L.ring + (unsigned)nst * (unsigned)D * 256u;
+    // full[nst], empty[nst], q full and empty, S, P and O full [2 each], done, parts written and merge
+    // decided [2 each], TMEM address, abort, merge[2]
+    L.total = L.bars + (2u * kChunkMaxStages + 13u) * 8u + 32u + 1024u;  // + alignment slack
+    return L;
+}
+
+// The rows whose values are not finite for a reason that may lie in keys they do not see (the MMA
+// multiplies a masked value by a zero weight, and 0 * inf is not 0): row by row, a warp per row, only
+// the keys [k0, k1) that the row sees. Never taken for finite values. Lane's dims: [lane * D / 32, + D / 32).
+template <int D>
+__device__ __forceinline__ void chunk_row_again(const ChunkArgs &a, int s, int lr, int g, const uint16_t *q, int k0, int k1,
+                                             float (&acc)[D / 32], float &m, float &l) {
+    constexpr int E = D / 32;
+    constexpr unsigned FULL = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    const float NEG_INF = __int_as_float(0xff800000);
+    float qv[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        qv[e] = __uint_as_float((unsigned)q[lane * E + e] << 16);
+        acc[e] = 0.f;
+    }
+    m = NEG_INF;
+    l = 0.f;
+    for (int j = k0; j < k1; ++j) {
+        long long row;
+        if (a.paged) {
+            const int pg = __ldg(a.block_table + (long long)s * a.max_pages + j / a.page_size);
+            row = (((long long)lr * a.n_pages + pg) * a.n_kv + g) * (long long)a.page_size + j % a.page_size;
+        } else {
+            row = (((long long)lr * a.batch + s) * a.n_kv + g) * (long long)a.cap_u + j;
+        }
+        float x = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) x += qv[e] * __uint_as_float((unsigned)a.K[row * D + lane * E + e] << 16);
+        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
+        x *= a.c;
+        const float mn = fmaxf(m, x);
+        const float corr = m == mn ? 1.f : ex2_approx(m - mn);
+        const float p = ex2_approx(x - (mn == NEG_INF ? 0.f : mn));
+        l = l * corr + p;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] = acc[e] * corr + p * __uint_as_float((unsigned)a.V[row * D + lane * E + e] << 16);
+        m = mn;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    tri_chunk_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const ChunkArgs a) {
+    constexpr int KCH = D / 64;                       // 64-dim (128-byte) chunks of a row
+    constexpr unsigned kTileBytes = (unsigned)D * 256u;
+    constexpr unsigned kChunkBytes = 128u * 128u;
+    constexpr unsigned FULL = 0xffffffffu;
+    const float NEG_INF = __int_as_float(0xff800000);
+    extern __shared__ unsigned char chunk_smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(chunk_smem_raw) + 1023) &
+                                                            ~uintptr_t(1023));
+    const int nst = a.nst;
+    const ChunkSmem Ly = chunk_smem(D, nst);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Ly.bars);
+    uint64_t *empty = full + kChunkMaxStages;
+    uint64_t *qfull = empty + kChunkMaxStages;
+    uint64_t *qempty = qfull + 1;
+    uint64_t *sfull = qempty + 1;   // [2]
+    uint64_t *pfull = sfull + 2;    // [2]
+    uint64_t *ofull = pfull + 2;    // [2]
+    uint64_t *done = ofull + 2;
+    uint64_t *parts = done + 1;     // [2]
+    uint64_t *decided = parts + 2;  // [2]
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(decided + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    volatile int *merge_flag = abort_flag + 1;        // [2]
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < nst; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        mbar_init(qfull, 1);
+        mbar_init(qempty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sfull + i, 1);
+            mbar_init(pfull + i, 4);  // the warpgroup's warps
+            mbar_init(ofull + i, 1);
+            mbar_init(parts + i, 4);
+            mbar_init(decided + i, 1);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        mbar_init_fence();
+    }
+    if (warp == 1) {  // one CTA per SM: the whole tensor memory
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                     "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    // a programmatic dependent of the plan kernel: the plan is read after this
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    const int G = a.group, LH = a.n_layers * a.n_kv;
+    const long long n_items = (long long)a.head->n_entries * LH;
+    // this CTA's item of round r: forth in even rounds, back in odd ones
+    auto item_of = [&](int r) {
+        const int pos = (r & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
+        return (long long)r * gridDim.x + pos;
+    };
+    auto fail = [&](const ChunkEntry &e, int lh) {
+        record_status(a.status, kDevTimeout, ((long long)(lh / a.n_kv) * a.batch + e.s) * a.n_kv + lh % a.n_kv);
+        *abort_flag = 1;
+    };
+
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChunkRegsFew));
+    if (warp == 0) {
+        // ---------------- loads ----------------
+        int k = 0, nq = 0;      // ring fills so far, query tiles loaded so far
+        bool ok = true;
+        for (int r = 0; ok && !*abort_flag; ++r) {
+            const long long it = item_of(r);
+            if (it >= n_items) break;
+            const ChunkEntry e = a.entries[it / LH];
+            const int lh = (int)(it % LH), lr = lh / a.n_kv, g = lh % a.n_kv;
+            if (e.kt1 <= e.kt0) continue;
+            const int ntile = e.ntok * G > 128 ? 2 : 1;
+            if (nq > 0 && !__all_sync(FULL, mbar_wait_bounded(qempty, (unsigned)((nq - 1) & 1), a.wait_tries))) {
+                if (lane == 0) fail(e, lh);
+                break;
+            }
+            if (lane == 0) {
+                mbar_expect_tx(qfull, (unsigned)ntile * kTileBytes);
+                for (int q = 0; q < ntile; ++q)
+                    for (int c = 0; c < KCH; ++c)
+                        tma_tile_4d(smem + Ly.q + q * kTileBytes + c * kChunkBytes, &qmap, c * 64, g * G,
+                                    e.tok0 + q * (128 / G), lr, qfull);
+            }
+            ++nq;
+            const int pr = a.piece_rows, np = 128 / pr;
+            const int p = lane / KCH, c = lane % KCH;  // this lane's box of a tile
+            const bool withhold = e.kt0 == 0 && ((long long)lr * a.batch + e.s) * a.n_kv + g == a.inject_unit;
+            auto page_of = [&](int kt) {
+                const int r0 = kt * 128 + p * pr;
+                return (a.paged && p < np && r0 < e.len)
+                           ? __ldg(a.block_table + (long long)e.s * a.max_pages + r0 / a.page_size) : 0;
+            };
+            int page = page_of(e.kt0);
+            for (int kt = e.kt0; kt < e.kt1 && ok; ++kt) {
+                const int r0 = kt * 128 + p * pr;
+                const bool mine = p < np && r0 < e.len;
+                long long row;
+                if (a.paged)
+                    row = (((long long)lr * a.n_pages + page) * a.n_kv + g) * (long long)a.page_size + r0 % a.page_size;
+                else
+                    row = (((long long)lr * a.batch + e.s) * a.n_kv + g) * (long long)a.cap_u + r0;
+                if (kt + 1 < e.kt1) page = page_of(kt + 1);
+                const int pieces = min(np, (e.len - kt * 128 + pr - 1) / pr);
+                for (int kv = 0; kv < 2; ++kv, ++k) {
+                    const int st = k % nst;
+                    if (k >= nst &&
+                        !__all_sync(FULL, mbar_wait_bounded(empty + st, (unsigned)((k / nst - 1) & 1), a.wait_tries))) {
+                        if (lane == 0) fail(e, lh);
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        // the MMA warp may have written zeros to this stage (generic proxy)
+                        fence_proxy_async_smem();
+                        mbar_expect_tx(full + st, (unsigned)(pieces * pr) * 128u * KCH);
+                    }
+                    __syncwarp();
+                    // test hook: the unit's first key tile is armed but never loaded
+                    if (mine && !(withhold && kt == 0 && kv == 0))
+                        tma_tile_2d(smem + Ly.ring + (unsigned)st * kTileBytes + c * kChunkBytes + (unsigned)(p * pr) * 128u,
+                                    kv ? &vmap : &kmap, c * 64, (int)row, full + st);
+                }
+            }
+        }
+        // copies still in flight must land before the CTA exits
+        for (int j = k > nst ? k - nst : 0; j < k; ++j)
+            (void)mbar_wait_bounded(full + j % nst, (unsigned)((j / nst) & 1), a.wait_tries);
+        if (nq > 0) (void)mbar_wait_bounded(qfull, (unsigned)((nq - 1) & 1), a.wait_tries);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------- MMAs ----------------
+        const uint32_t id_s = mx_idesc(128), id_o = mx_idesc(D) | (1u << 16);  // V is N-major
+        const uint32_t q_low = desc_low(smem_u32(smem + Ly.q), 16u), k_low = desc_low(smem_u32(smem + Ly.ring), 16u);
+        const uint32_t v_low = desc_low(smem_u32(smem + Ly.ring), kChunkBytes);
+        int k = 0, nq = 0, np[2] = {0, 0};  // tiles consumed, items, P tiles taken
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, unsigned phase) {
+            return __all_sync(FULL, mbar_wait_bounded(bar, phase & 1u, a.wait_tries));
+        };
+        for (int r = 0; ok && !*abort_flag; ++r) {
+            const long long it = item_of(r);
+            if (it >= n_items) break;
+            const ChunkEntry e = a.entries[it / LH];
+            const int lh = (int)(it % LH);
+            const int n = e.kt1 - e.kt0;
+            if (n <= 0) continue;
+            const int ntile = e.ntok * G > 128 ? 2 : 1;
+            auto mma_s = [&](int q, int st) {
+                const uint32_t al = q_low + q * (kTileBytes >> 4), bl = k_low + (unsigned)st * (kTileBytes >> 4);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const unsigned off = ((unsigned)(ks >> 2) * kChunkBytes + (unsigned)(ks & 3) * 32u) >> 4;
+                    chunk_mma_ss(tmem + 128u * q, al + off, bl + off, id_s, ks > 0);
+                }
+                mx_commit(sfull + q);
+            };
+            ok = wait(qfull, nq) && wait(full + k % nst, k / nst);
+            if (!ok) {
+                if (lane == 0) fail(e, lh);
+                break;
+            }
+            ++nq;
+            tc_fence_after();
+            if (lane == 0) {
+                for (int q = 0; q < ntile; ++q) mma_s(q, k % nst);
+                mx_commit(empty + k % nst);
+                if (n == 1) mx_commit(qempty);
+            }
+            __syncwarp();
+            ++k;
+            for (int i = 0; i < n && ok; ++i) {
+                const int sv = k % nst, sk = (k + 1) % nst;  // this tile's V, the next tile's K
+                ok = wait(full + sv, k / nst);
+                if (!ok) break;
+                // value rows past the length hold whatever was there: zero them, for a zero weight does
+                // not clear a NaN
+                const int valid = e.len - (e.kt0 + i) * 128;
+                if (valid < 128) {
+                    unsigned char *Vs = smem + Ly.ring + (unsigned)sv * kTileBytes;
+                    const int words = (128 - valid) * 8;  // 16-byte words of a chunk
+                    for (int w = lane; w < words * KCH; w += 32) {
+                        const int c = w / words, x = w % words;
+                        *reinterpret_cast<uint4 *>(Vs + c * kChunkBytes + (unsigned)valid * 128u + (unsigned)x * 16u) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                for (int q = 0; q < ntile; ++q) {
+                    ok = ok && wait(pfull + q, np[q]);
+                    if (!ok) break;
+                    ++np[q];
+                    if (i + 1 < n && q == 0) ok = wait(full + sk, (k + 1) / nst);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t vl = v_low + (unsigned)sv * (kTileBytes >> 4);
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)  // 16 keys: 16 rows of 128 bytes of each chunk
+                            chunk_mma_ts(tmem + 256u + (uint32_t)(D * q), tmem + 128u * q + 8u * ks, vl + ks * 128u, id_o,
+                                         (i > 0 || ks > 0));
+                        if (i + 1 < n) mma_s(q, sk);
+                        else mx_commit(ofull + q);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (lane == 0) {
+                    mx_commit(empty + sv);
+                    if (i + 1 < n) mx_commit(empty + sk);
+                    if (i + 2 == n) mx_commit(qempty);
+                }
+                __syncwarp();
+                k += i + 1 < n ? 2 : 1;
+            }
+            if (!ok) {
+                if (lane == 0) fail(e, lh);
+                break;
+            }
+        }
+        // MMAs may still run (after a wait that ran out): they must end before the TMEM is released
+        if (lane == 0) mx_commit(done);
+        __syncwarp();
+        (void)mbar_wait_bounded(done, 0u, a.wait_tries);
+        __syncwarp();
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChunkRegsMany));
+        // ---------------- softmax: warpgroup q, one row per thread ----------------
+        const int q = (warp - 4) >> 2;
+        const int row = (warp & 3) * 32 + lane;          // TMEM lane
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + 128u * q, to = tmem + lanes + 256u + (uint32_t)(D * q);
+        const int wg_tid = tid & 127;
+        unsigned ns = 0, no = 0, nm = 0;                  // S tiles, items, items in parts so far
+        bool ok = true;
+        for (int r = 0; ok && !*abort_flag; ++r) {
+            const long long it = item_of(r);
+            if (it >= n_items) break;
+            const ChunkEntry e = a.entries[it / LH];
+            const int lh = (int)(it % LH), lr = lh / a.n_kv, g = lh % a.n_kv;
+            const int n = e.kt1 - e.kt0;
+            const int rows = e.ntok * G - 128 * q;        // rows of this tile
+            if (rows <= 0) continue;
+            const int tok = (128 * q + row) / G, hd = (128 * q + row) % G;
+            const bool mine = row < rows;
+            const int limit = min(e.len, a.causal ? e.first + tok : e.len);
+            const int sure = min(e.len, a.causal ? e.first + 128 * q / G : e.len);  // seen by every row
+            float m = NEG_INF, l = 0.f;
+            for (int i = 0; i < n; ++i) {
+                ok = __all_sync(FULL, mbar_wait_bounded(sfull + q, ns & 1u, a.wait_tries));
+                if (!ok) break;
+                ++ns;
+                tc_fence_after();
+                uint32_t s0[32], s1[32], s2[32], s3[32];
+                tmem_ld32(ts, s0);
+                tmem_ld32(ts + 32u, s1);
+                tmem_ld32(ts + 64u, s2);
+                tmem_ld32(ts + 96u, s3);
+                tmem_wait32(s0);
+                tmem_after32(s1);
+                tmem_after32(s2);
+                tmem_after32(s3);
+                const int key0 = (e.kt0 + i) * 128;
+                if (key0 + 128 > sure) {
+                    const int left = limit - key0;        // columns that this row sees
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        if (j >= left) s0[j] = 0xff800000u;
+                        if (j + 32 >= left) s1[j] = 0xff800000u;
+                        if (j + 64 >= left) s2[j] = 0xff800000u;
+                        if (j + 96 >= left) s3[j] = 0xff800000u;
+                    }
+                }
+                float x0 = NEG_INF, x1 = NEG_INF, x2 = NEG_INF, x3 = NEG_INF;
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    x0 = max3f(x0, __uint_as_float(s0[j]), __uint_as_float(s0[j + 1]));
+                    x1 = max3f(x1, __uint_as_float(s1[j]), __uint_as_float(s1[j + 1]));
+                    x2 = max3f(x2, __uint_as_float(s2[j]), __uint_as_float(s2[j + 1]));
+                    x3 = max3f(x3, __uint_as_float(s3[j]), __uint_as_float(s3[j + 1]));
+                }
+                const float mx = fmaxf(max3f(x0, x1, x2), x3);
+                if (i == 0) {
+                    m = mx;
+                } else if (__any_sync(FULL, (mx - m) * a.c > 8.f)) {
+                    // P V of the tiles before is complete: O is this warpgroup's to rescale
+                    const float mn = fmaxf(m, mx);
+                    const float f = m == mn ? 1.f : ex2_approx((m - mn) * a.c);
+                    m = mn;
+                    l *= f;
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(to + c0, o);
+                        tmem_wait32(o);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_st32(to + c0, o);
+                    }
+                }
+                const float mc = m == NEG_INF ? 0.f : m * a.c;
+                float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+                auto weights = [&](const uint32_t(&s)[32], uint32_t *p) {
+                    const float2 c2 = make_float2(a.c, a.c), m2 = make_float2(-mc, -mc);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        float2 y0 = __ffma2_rn(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), c2, m2);
+                        float2 y1 = __ffma2_rn(make_float2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), c2, m2);
+                        y0 = make_float2(ex2_approx(y0.x), ex2_approx(y0.y));
+                        y1 = make_float2(ex2_approx(y1.x), ex2_approx(y1.y));
+                        sum0 = __fadd2_rn(sum0, y0);
+                        sum1 = __fadd2_rn(sum1, y1);
+                        p[j / 2] = pack_bf16(y0.x, y0.y);
+                        p[j / 2 + 1] = pack_bf16(y1.x, y1.y);
+                    }
+                };
+                uint32_t p[32];
+                weights(s0, p);
+                weights(s1, p + 16);
+                tmem_st32(ts, p);
+                weights(s2, p);
+                weights(s3, p + 16);
+                tmem_st32(ts + 32u, p);
+                l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pfull + q);
+            }
+            if (!ok) {
+                if (lane == 0) fail(e, lh);
+                break;
+            }
+            if (n > 0) {
+                ok = __all_sync(FULL, mbar_wait_bounded(ofull + q, no & 1u, a.wait_tries));
+                if (!ok) {
+                    if (lane == 0) fail(e, lh);
+                    break;
+                }
+                ++no;
+                tc_fence_after();
+            }
+            // ---- the result of the item, or its part ----
+            const long long trow = e.tok0 + tok;
+            const int head = g * G + hd;
+            uint16_t *orow = a.out + lr * a.o_l + trow * a.o_t + head * a.o_h;
+            const long long slot = ((long long)e.slot * LH + (long long)lh * e.nsplit + e.split) * 2 + q;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            float lse = NEG_INF;
+            if (l != 0.f) lse = (m * a.c + log2f(l)) * 0.6931471805599453f;
+            bool odd = false;
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld32(to + c0, o);
+                    tmem_wait32(o);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = 0u;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) odd |= (o[j] & 0x7f800000u) == 0x7f800000u;
+                if (e.nsplit == 1) {
+                    if (mine) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            uint4 w;
+                            w.x = pack_bf16(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
+                            w.y = pack_bf16(__uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+                            w.z = pack_bf16(__uint_as_float(o[j + 4]) * inv, __uint_as_float(o[j + 5]) * inv);
+                            w.w = pack_bf16(__uint_as_float(o[j + 6]) * inv, __uint_as_float(o[j + 7]) * inv);
+                            *reinterpret_cast<uint4 *>(orow + c0 + j) = w;
+                        }
+                    }
+                } else if (mine) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<float4 *>(a.part + ((slot * (D / 4) + (c0 + j) / 4) * 128 + row) * 4) =
+                            make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]), __uint_as_float(o[j + 2]),
+                                        __uint_as_float(o[j + 3]));
+                }
+            }
+            tc_fence_before();
+            if (mine) {
+                if (e.nsplit > 1)
+                    *reinterpret_cast<float2 *>(a.part_ml + (slot * 128 + row) * 2) = make_float2(m * a.c, l);
+                else if (a.lse)
+                    a.lse[((long long)lr * a.n_tokens + trow) * (a.n_kv * G) + head] = lse;
+            }
+            unsigned again = __ballot_sync(FULL, mine && odd && limit < min(e.len, e.kt1 * 128));
+            __syncwarp();
+            while (again) {  // see chunk_row_again
+                const int src = __ffs(again) - 1;
+                again &= again - 1;
+                const int rt = __shfl_sync(FULL, tok, src), rh = __shfl_sync(FULL, hd, src), rl = __shfl_sync(FULL, limit, src);
+                float acc[D / 32], rm, rs;
+                chunk_row_again<D>(a, e.s, lr, g, a.q + lr * a.q_l + (e.tok0 + rt) * a.q_t + (g * G + rh) * a.q_h,
+                                   e.kt0 * 128, min(rl, e.kt1 * 128), acc, rm, rs);
+                const int rr = (warp & 3) * 32 + src;
+                if (e.nsplit == 1) {
+                    uint16_t *dst = a.out + lr * a.o_l + (e.tok0 + rt) * a.o_t + (g * G + rh) * a.o_h;
+                    const float ri = rs == 0.f ? 0.f : 1.f / rs;
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x)
+                        dst[lane * (D / 32) + x] = (uint16_t)(pack_bf16(rs == 0.f ? 0.f : acc[x] * ri, 0.f) & 0xffffu);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x) {
+                        const int dim = lane * (D / 32) + x;
+                        a.part[((slot * (D / 4) + dim / 4) * 128 + rr) * 4 + dim % 4] = acc[x];
+                    }
+                    if (lane == 0) *reinterpret_cast<float2 *>(a.part_ml + (slot * 128 + rr) * 2) = make_float2(rm, rs);
+                }
+                __syncwarp();
+            }
+            if (e.nsplit > 1) {
+                // the last part of the block to arrive merges them all, in the order of the keys
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(parts + q);
+                ok = __all_sync(FULL, mbar_wait_bounded(parts + q, nm & 1u, a.wait_tries));
+                if (ok && wg_tid == 0) {
+                    const long long grp = ((long long)e.group * LH + lh) * 2 + q;
+                    merge_flag[q] = atomicAdd(a.counters + grp, 1u) == (unsigned)e.nsplit - 1;
+                    __threadfence();
+                    mbar_arrive(decided + q);
+                }
+                __syncwarp();
+                ok = ok && __all_sync(FULL, mbar_wait_bounded(decided + q, nm & 1u, a.wait_tries));
+                if (!ok) {
+                    if (lane == 0) fail(e, lh);
+                    break;
+                }
+                ++nm;
+                // the flag is written again only after every warp has arrived with its next part
+                if (merge_flag[q]) {
+                    const long long first = ((long long)e.slot * LH + (long long)lh * e.nsplit) * 2 + q;
+                    const int nv = min(128, rows);
+                    for (int x = wg_tid; x < nv * (D / 4); x += 128) {
+                        const int rr = x % nv, c4 = x / nv;
+                        float M = NEG_INF;
+                        for (int k = 0; k < e.nsplit; ++k) {
+                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + ((first + 2 * k) * 128 + rr) * 2));
+                            M = fmaxf(M, ml.x);
+                        }
+                        float L = 0.f;
+                        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int k = 0; k < e.nsplit; ++k) {
+                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + ((first + 2 * k) * 128 + rr) * 2));
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+                                a.part + (((first + 2 * k) * (D / 4) + c4) * 128 + rr) * 4));
+                            const float w = ml.y == 0.f ? 0.f : ex2_approx(ml.x - M);
+                            if (ml.y != 0.f) {  // a part that sees no key of the row weighs nothing
+                                L += ml.y * w;
+                                A.x += v.x * w;
+                                A.y += v.y * w;
+                                A.z += v.z * w;
+                                A.w += v.w * w;
+                            }
+                        }
+                        const float li = L == 0.f ? 0.f : 1.f / L;
+                        const int rt = (128 * q + rr) / G, rh = g * G + (128 * q + rr) % G;
+                        uint2 w;
+                        w.x = pack_bf16(A.x * li, A.y * li);
+                        w.y = pack_bf16(A.z * li, A.w * li);
+                        *reinterpret_cast<uint2 *>(a.out + lr * a.o_l + (e.tok0 + rt) * a.o_t + rh * a.o_h + 4 * c4) = w;
+                        if (c4 == 0 && a.lse)
+                            a.lse[((long long)lr * a.n_tokens + e.tok0 + rt) * (a.n_kv * G) + rh] =
+                                L == 0.f ? NEG_INF : (M + log2f(L)) * 0.6931471805599453f;
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    }
+}
+
+}  // namespace tri

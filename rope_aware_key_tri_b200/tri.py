@@ -22,8 +22,10 @@ LIB_PATH = os.path.join(_HERE, "lib", "libtri_b200.so")
 TRI_OK, TRI_EINVAL, TRI_ENOMEM, TRI_ECUDA, TRI_ESTATE, TRI_EDEVICE, TRI_EUNSUPPORTED = range(7)
 TRI_ROPE_HALF, TRI_ROPE_INTERLEAVED = 0, 1
 TRI_OFFSETS_MEAN, TRI_OFFSETS_MAX = 0, 1
+TRI_ROPE_PLAIN, TRI_ROPE_LINEAR, TRI_ROPE_NTK, TRI_ROPE_YARN, TRI_ROPE_SMOOTH = range(5)
 TRI_ENGINE_AUTO, TRI_ENGINE_CUDA_CORES, TRI_ENGINE_TENSOR = 0, 1, 2
 TRI_DEV_NONE, TRI_DEV_LEN_GT_CAP, TRI_DEV_BAD_PAGE, TRI_DEV_TIMEOUT, TRI_DEV_INTERNAL, TRI_DEV_T_NOT_AFTER_POS = range(6)
+TRI_DEV_BAD_RANGE = 6
 
 
 class tri_kv(ctypes.Structure):
@@ -41,6 +43,15 @@ class tri_kv(ctypes.Structure):
         ("n_pages", ctypes.c_int32),
         ("layer_begin", ctypes.c_int32),
         ("n_layers", ctypes.c_int32),
+    ]
+
+
+class tri_rows(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("layer_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
     ]
 
 
@@ -72,6 +83,12 @@ def _load():
     L.tri_get_failed_units.argtypes = [P, P, P, I32, ctypes.POINTER(I32)]
     L.tri_decode_attention.argtypes = [P, ctypes.POINTER(tri_kv), P, P, P]
     L.tri_set_test_fault.argtypes = [P, I64, I32]
+    R = ctypes.POINTER(tri_rows)
+    L.tri_rope_frequencies.argtypes = [ctypes.c_int, D, ctypes.c_int, D, D, D, D, P, ctypes.POINTER(D)]
+    L.tri_rope_load.argtypes = [P, ctypes.c_int, ctypes.c_int, P, D]
+    L.tri_rope.argtypes = [P, R, R, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, P, ctypes.c_int, P]
+    L.tri_append_chunk.argtypes = [P, ctypes.POINTER(tri_kv), R, R, P, P, ctypes.c_int, ctypes.c_int, R, R, P]
+    L.tri_chunk_attention.argtypes = [P, ctypes.POINTER(tri_kv), R, P, ctypes.c_int, D, ctypes.c_int, R, P, P]
     L.tri_set_tuning.argtypes = [P, ctypes.c_int, ctypes.c_int]
     L.tri_set_offset_combine.argtypes = [P, ctypes.c_int]
     L.tri_set_score_engine.argtypes = [P, ctypes.c_int]
@@ -83,6 +100,7 @@ def _load():
                "tri_calibrate_estimate", "tri_append", "tri_append_advance", "tri_get_error", "tri_set_tuning",
                "tri_set_offset_combine",
                "tri_get_failed_units", "tri_set_test_fault", "tri_decode_attention", "tri_set_score_engine",
+               "tri_rope_frequencies", "tri_rope_load", "tri_rope", "tri_append_chunk", "tri_chunk_attention",
                "tri_version"):
         getattr(L, fn).restype = ctypes.c_int
     return L
@@ -160,6 +178,46 @@ def tri_append(ctx, kv: tri_kv, k_new_ptr: int, v_new_ptr: int, pos_new_ptr: int
 
 def tri_append_advance(ctx, kv: tri_kv, k_new_ptr: int, v_new_ptr: int, pos_ptr: int, stream: int) -> int:
     return _lib.tri_append_advance(ctx, ctypes.byref(kv), k_new_ptr, v_new_ptr, pos_ptr, stream)
+
+
+_SCALINGS = {"plain": TRI_ROPE_PLAIN, "linear": TRI_ROPE_LINEAR, "ntk": TRI_ROPE_NTK, "yarn": TRI_ROPE_YARN,
+             "smooth": TRI_ROPE_SMOOTH}
+
+
+def rope_frequencies(rotary_dim, base, scaling="plain", factor=1.0, original_length=0.0, low=1.0, high=32.0):
+    """(omega fp64 [rotary_dim/2], magnitude) for :meth:`TriContext.rope_load`: "plain", "linear", "ntk", "yarn" or
+    "smooth" (or the TRI_ROPE_* value). Host only."""
+    omega = np.empty(max(0, int(rotary_dim)) // 2, dtype=np.float64)
+    mag = ctypes.c_double()
+    st = _lib.tri_rope_frequencies(int(rotary_dim), float(base), int(_SCALINGS.get(scaling, scaling)), float(factor),
+                                   float(original_length), float(low), float(high), omega.ctypes.data, ctypes.byref(mag))
+    if st != TRI_OK:
+        raise TriError(st, "tri_rope_frequencies")
+    return omega, mag.value
+
+
+def tri_rope_load(ctx, rotary_dim: int, layout: int, omega, magnitude: float) -> int:
+    om = np.ascontiguousarray(omega, dtype=np.float64)
+    return _lib.tri_rope_load(ctx, int(rotary_dim), int(layout), om.ctypes.data, float(magnitude))
+
+
+def tri_rope(ctx, x: tri_rows, out: tri_rows, n_layers: int, n_tokens: int, n_heads: int, head_dim: int, pos_ptr: int,
+             inverse: int, stream: int) -> int:
+    return _lib.tri_rope(ctx, ctypes.byref(x), ctypes.byref(out), int(n_layers), int(n_tokens), int(n_heads), int(head_dim),
+                         pos_ptr, int(inverse), stream)
+
+
+def tri_append_chunk(ctx, kv: tri_kv, K_new: tri_rows, V_new: tri_rows, cu_ptr: int, pos_ptr: int, n_tokens: int,
+                     rotate: int, q: Optional[tri_rows], q_out: Optional[tri_rows], stream: int) -> int:
+    return _lib.tri_append_chunk(ctx, ctypes.byref(kv), ctypes.byref(K_new), ctypes.byref(V_new), cu_ptr, pos_ptr,
+                                 int(n_tokens), int(rotate), None if q is None else ctypes.byref(q),
+                                 None if q_out is None else ctypes.byref(q_out), stream)
+
+
+def tri_chunk_attention(ctx, kv: tri_kv, q: tri_rows, cu_ptr: int, n_tokens: int, scale: float, causal: int,
+                        out: tri_rows, lse_ptr: Optional[int], stream: int) -> int:
+    return _lib.tri_chunk_attention(ctx, ctypes.byref(kv), ctypes.byref(q), cu_ptr, int(n_tokens), float(scale),
+                                    int(causal), ctypes.byref(out), lse_ptr, stream)
 
 
 def tri_get_error(ctx, stream: int):
@@ -254,12 +312,37 @@ def make_kv(K, V, pos, lens, lens_out=None, block_table=None, n_pages=None, laye
     return kv
 
 
+def make_rows(x: torch.Tensor, name: str = "x") -> tri_rows:
+    """Describe bf16 rows held in a torch tensor [tokens][heads][d] or [layers][tokens][heads][d]: any strides that are
+    multiples of 8 elements, each row contiguous."""
+    if x.dtype != torch.bfloat16 or not x.is_cuda or x.dim() not in (3, 4):
+        raise ValueError(f"{name} must be a CUDA tensor of torch.bfloat16 [tokens][heads][d] or [layers][tokens][heads][d]")
+    shape, stride = x.shape, x.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    r = tri_rows()
+    r.data = x.data_ptr()
+    # a dimension of one element has no stride of its own
+    r.head_stride = stride[-2] if shape[-2] > 1 else 0
+    r.token_stride = stride[-3] if shape[-3] > 1 else 0
+    r.layer_stride = stride[0] if len(shape) == 4 and shape[0] > 1 else 0
+    return r
+
+
 class TriContext:
     """One library context on one CUDA device."""
 
     def __init__(self, device: int = 0):
         self.device = int(device)
         self.handle = tri_create(self.device)
+        self.shape = None  # (n_layers, n_kv_heads, group, head_dim) of the loaded statistics
+
+    def _heads(self, name, q, n_kv):
+        # the C ABI takes the head counts from the statistics: what the tensors hold must agree
+        if self.shape is not None and (int(q.shape[-2]), n_kv, int(q.shape[-1])) != (
+                self.shape[1] * self.shape[2], self.shape[1], self.shape[3]):
+            raise ValueError(f"{name} and the cache have {q.shape[-2]} and {n_kv} heads of {q.shape[-1]}, the loaded "
+                             f"statistics {self.shape[1] * self.shape[2]} and {self.shape[1]} of {self.shape[3]}")
 
     def close(self):
         if self.handle is not None:
@@ -278,6 +361,7 @@ class TriContext:
                                 q_mean, q_norm_mean, R, offsets)
         if st != TRI_OK:
             raise TriError(st, "tri_calibrate_load")
+        self.shape = (int(n_layers), int(n_kv_heads), int(group), int(head_dim))
 
     def set_offset_combine(self, combine):
         """"mean" (the default) or "max" over the future offsets (or the TRI_OFFSETS_* value)."""
@@ -369,6 +453,101 @@ class TriContext:
             return st
         if st != TRI_OK:
             raise TriError(st, "tri_decode_attention", tri_last_error(self.handle))
+        return out
+
+    def _vector(self, name, x, n):
+        if x.dtype != torch.int32 or not x.is_cuda or not x.is_contiguous() or x.dim() != 1 or x.shape[0] != n:
+            raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of {n} elements, got {tuple(x.shape)} {x.dtype}")
+        return x.data_ptr()
+
+    def _here(self, **tensors):
+        for name, x in tensors.items():
+            if x is not None and x.device.index != self.device:
+                raise ValueError(f"{name} is on {x.device}, the context on cuda:{self.device}")
+
+    def _stream(self, stream):
+        return (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+
+    def rope_load(self, omega, layout, magnitude=1.0):
+        """The rotation of :meth:`rope` and :meth:`append_chunk`: omega fp64 [rotary_dim/2] radians per position (e.g. of
+        :func:`rope_frequencies`), TRI_ROPE_HALF or TRI_ROPE_INTERLEAVED, and the magnitude of the rotated dims."""
+        st = tri_rope_load(self.handle, 2 * len(omega), layout, omega, magnitude)
+        if st != TRI_OK:
+            raise TriError(st, "tri_rope_load", tri_last_error(self.handle))
+
+    def rope(self, x, pos, out=None, inverse=False, stream=None, check=True):
+        """Rotate the rows x (bf16 [tokens][heads][d] or [layers][tokens][heads][d], see make_rows) at pos (int32 [tokens]);
+        inverse=True rotates back. Returns out (x itself is accepted), or the status when check is False."""
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if out.shape != x.shape:
+            raise ValueError(f"out must be shaped like x {tuple(x.shape)}, got {tuple(out.shape)}")
+        self._here(x=x, pos=pos, out=out)
+        rows, rout = make_rows(x, "x"), make_rows(out, "out")
+        T, H, d = x.shape[-3:]
+        st = tri_rope(self.handle, rows, rout, x.shape[0] if x.dim() == 4 else 1, T, H, d, self._vector("pos", pos, T),
+                      inverse, self._stream(stream))
+        if not check:
+            return st
+        if st != TRI_OK:
+            raise TriError(st, "tri_rope", tri_last_error(self.handle))
+        return out
+
+    def _tokens(self, name, x, L, T, heads, d):
+        if (tuple(x.shape[-3:]) != (T, heads, d) if heads else x.shape[-1] != d) or (x.shape[0] if x.dim() == 4 else 1) != L:
+            raise ValueError(f"{name} must be [{L} layers][{T} tokens][{heads or 'heads'}][{d}], got {tuple(x.shape)}")
+        return make_rows(x, name)
+
+    def append_chunk(self, K, V, pos, lens, K_new, V_new, cu_new, pos_new, block_table=None, lens_out="inplace",
+                     rotate=True, q=None, q_out=None, n_pages=None, layer_begin=0, stream=None, check=True):
+        """Append runs of new tokens to a cache (see make_kv for the layouts). K_new, V_new: bf16 rows
+        [n_layers][tokens][n_kv_heads][d] (or without layers for one; strided views are accepted), sequence s holding the
+        tokens [cu_new[s], cu_new[s + 1]); pos_new int32 [tokens]. rotate: K_new is pre-RoPE and rotated on the way; q
+        (rows of the query heads) is then rotated into q_out in the same launch (q_out=None: in place)."""
+        if isinstance(lens_out, str):
+            lens_out = lens
+        kv = make_kv(K, V, pos, lens, lens_out, block_table, n_pages=n_pages, layer_begin=layer_begin)
+        L, H, d, T, B = int(K.shape[0]), int(K.shape[2]), int(K.shape[4]), int(K_new.shape[-3]), int(lens.shape[0])
+        self._here(K=K, V=V, pos=pos, lens=lens, lens_out=lens_out, block_table=block_table, K_new=K_new, V_new=V_new,
+                   cu_new=cu_new, pos_new=pos_new, q=q, q_out=q_out)
+        kn, vn = self._tokens("K_new", K_new, L, T, H, d), self._tokens("V_new", V_new, L, T, H, d)
+        if lens_out is not None and lens_out.shape != lens.shape:
+            raise ValueError("lens_out must be shaped like lens")
+        qr = qo = None
+        if q is not None:
+            q_out = q if q_out is None else q_out
+            if q_out.shape != q.shape or q.shape[-2] % H:
+                raise ValueError(f"q_out must be shaped like q {tuple(q.shape)}, its heads a multiple of {H}")
+            qr, qo = self._tokens("q", q, L, T, int(q.shape[-2]), d), self._tokens("q_out", q_out, L, T, int(q.shape[-2]), d)
+            self._heads("q", q, H)
+        st = tri_append_chunk(self.handle, kv, kn, vn, self._vector("cu_new", cu_new, B + 1),
+                              self._vector("pos_new", pos_new, T), T, bool(rotate), qr, qo, self._stream(stream))
+        if check and st != TRI_OK:
+            raise TriError(st, "tri_append_chunk", tri_last_error(self.handle))
+        return st
+
+    def chunk_attention(self, K, V, lens, q, cu_q, out=None, lse=None, scale=None, causal=True, block_table=None,
+                        n_pages=None, layer_begin=0, stream=None, check=True):
+        """Attention of the post-RoPE queries q (bf16 rows [n_layers][tokens][Hq][d], or without layers for one;
+        sequence s holding the tokens [cu_q[s], cu_q[s + 1])) over the cache that already holds those tokens as the
+        last of its lens[s] rows. scale: of the logits (None: 1/sqrt(d)); lse: fp32 [n_layers][tokens][Hq] to receive
+        the logarithm of the softmax sums. Returns out (bf16, like q), or the status when check is False."""
+        kv = make_kv(K, V, None, lens, None, block_table, n_pages=n_pages, layer_begin=layer_begin)
+        L, H, d, B = int(K.shape[0]), int(K.shape[2]), int(K.shape[4]), int(lens.shape[0])
+        T, Hq = int(q.shape[-3]), int(q.shape[-2])
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        self._here(K=K, V=V, lens=lens, block_table=block_table, q=q, cu_q=cu_q, out=out, lse=lse)
+        qr, ro = self._tokens("q", q, L, T, Hq, d), self._tokens("out", out, L, T, Hq, d)
+        self._heads("q", q, H)
+        if lse is not None and (lse.dtype != torch.float32 or lse.numel() != L * T * Hq or not lse.is_contiguous()):
+            raise ValueError(f"lse must be a contiguous float32 tensor [{L}][{T}][{Hq}]")
+        st = tri_chunk_attention(self.handle, kv, qr, self._vector("cu_q", cu_q, B + 1), T,
+                                 d ** -0.5 if scale is None else scale, bool(causal), ro, _ptr(lse), self._stream(stream))
+        if not check:
+            return st
+        if st != TRI_OK:
+            raise TriError(st, "tri_chunk_attention", tri_last_error(self.handle))
         return out
 
     def calibrate_estimate(self, Q, layout, out=None, stream=None, check=True):
