@@ -1452,7 +1452,7 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
     };
     const size_t o_head = take(sizeof(tri::ChunkHead)), o_seqs = take(sizeof(tri::ChunkSeq) * (size_t)kv->batch),
                  o_base = take(sizeof(int) * ((size_t)kv->batch + 1)), o_tiles = take(sizeof(int) * (size_t)blocks),
-                 o_per = take(sizeof(int) * (size_t)blocks), o_counters = take(sizeof(unsigned) * 2 * (size_t)a.max_slots),
+                 o_counters = take(sizeof(unsigned) * 2 * (size_t)a.max_slots),
                  o_entries = take(sizeof(tri::ChunkEntry) * (size_t)entries);
     const size_t part_floats = (size_t)a.max_slots * 2 * 128 * D, ml_floats = (size_t)a.max_slots * 2 * 128 * 2;
     const bool fresh = off > c->ws_plan.bytes;
@@ -1464,7 +1464,6 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
     a.seqs = reinterpret_cast<tri::ChunkSeq *>(ws + o_seqs);
     a.base = reinterpret_cast<int *>(ws + o_base);
     a.tiles = reinterpret_cast<int *>(ws + o_tiles);
-    a.per = reinterpret_cast<int *>(ws + o_per);
     a.counters = reinterpret_cast<unsigned *>(ws + o_counters);
     a.entries = reinterpret_cast<tri::ChunkEntry *>(ws + o_entries);
     a.part = static_cast<float *>(c->ws_part.p);
@@ -1486,10 +1485,7 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
         std::snprintf(c->last_error, sizeof c->last_error, "cuTensorMapEncodeTiled failed");
         return TRI_ECUDA;
     }
-    // ring: as many stages as fit beside the query tiles, which also keeps it to one CTA per SM (each
-    // allocates the whole tensor memory)
-    a.nst = D == 128 ? 5 : 8;
-    const unsigned smem = tri::chunk_smem(D, a.nst).total;
+    const unsigned smem = tri::chunk_smem(D).total;
     const void *fn = D == 128 ? (const void *)&tri::tri_chunk_kernel<128> : (const void *)&tri::tri_chunk_kernel<64>;
     ce = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (ce != cudaSuccess) return cuda_fail(c, ce, "cudaFuncSetAttribute(chunk)");

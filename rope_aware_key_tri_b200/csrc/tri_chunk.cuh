@@ -16,12 +16,12 @@
 // Items are handed out longest first, in rounds that run forth and back over the CTAs.
 //
 // The attention kernel, one persistent CTA per SM: warp 0 loads (TMA, 128-byte swizzle: the item's
-// query rows, then K and V tiles through a ring), warp 1 issues the tcgen05 MMAs, and two warpgroups
-// take one 128-row query tile each, a row per thread:
+// query rows, then K and V tiles through a ring), and two warpgroups take one 128-row query tile each,
+// a row per thread, with a warp each (1 and 2) that issues its tcgen05 MMAs:
 //   S_q = Q_q K^T            128 x 128 x D into TMEM columns [128 q, 128 q + 128)
 //   P_q = 2^((S_q - m) c)    read, masked, exponentiated, rounded to bf16 and written over S_q
 //   O_q += P_q V             A from TMEM, V as the N-major operand: the tile lies as it came
-// The MMA warp runs O_q += P_q V(i) and S_q = Q_q K(i+1)^T back to back, so that one warpgroup's
+// An MMA warp runs O_q += P_q V(i) and S_q = Q_q K(i+1)^T back to back, so that one warpgroup's
 // exponentials overlap the other's MMAs; S_q(i+1) complete implies P_q V(i) complete, so O_q is the
 // warpgroup's own until it hands over P_q(i+1): it rescales O_q itself, and only where the maximum
 // has grown by more than 2^8 since the last rescale (p then stays below 2^8; nothing is lost, the
@@ -47,22 +47,25 @@
 namespace tri {
 
 constexpr int kChunkRows = 256;     // packed query rows of an item: two MMA tiles
-constexpr int kChunkThreads = 384;  // a warpgroup with the load and the MMA warp, two for the softmax
+constexpr int kChunkThreads = 384;  // a warpgroup with the load and the MMA warps, two for the softmax
 // Registers a thread after the split: 128 * 72 + 256 * 216 = 64512, the 384 * 168 that the
 // block is launched with. A softmax thread holds a row of 128 logits.
 constexpr int kChunkRegsFew = 72, kChunkRegsMany = 216;
 constexpr int kChunkPlanThreads = 256;
-constexpr int kChunkMaxStages = 8;
+// Ring stages: as many as fit beside the query tiles, which also keeps it to one CTA per SM (each allocates
+// the whole tensor memory).
+__host__ __device__ constexpr int chunk_stages(int D) { return D == 128 ? 5 : 8; }
 
 // One line of the plan: a block of rows of one sequence over the key tiles [kt0, kt1), for every
 // layer and KV head.
 struct __align__(16) ChunkEntry {
     int s, tok0, ntok, len;   // sequence, first token (global row), tokens of the block, cached rows
     int first, kt0, kt1;      // keys seen by the block's first row, key tiles
-    int nsplit, split, slot, group, pad;  // splits of the block; this one; its first partial; its counter
+    int pair;                 // one row tile whose key tiles the two warpgroups take in turn
+    int nsplit, split, slot, group;  // splits of the block; this one; its first partial; its counter
 };
 
-struct ChunkSeq {
+struct __align__(16) ChunkSeq {
     int q0, n, len, bad;
 };
 
@@ -79,7 +82,6 @@ struct ChunkArgs {
     int paged, page_size, max_pages, n_pages, cap_u;
     int causal;
     int piece_rows;           // rows of a key box
-    int nst;                  // ring stages
     int sm_count, max_slots, max_entries;
     float c;                  // scale * log2(e)
     // where the query rows and results are (strides in elements)
@@ -94,7 +96,6 @@ struct ChunkArgs {
     ChunkSeq *seqs;           // [batch]
     int *base;                // [batch + 1] blocks before each sequence
     int *tiles;               // [max blocks] key tiles of each block
-    int *per;                 // (scratch of the plan) tiles of a split of each block
     ChunkEntry *entries;
     float *part;              // [slot][tile][D / 4][128][4], then [slot][tile][128][2] (m, l)
     float *part_ml;
@@ -106,19 +107,36 @@ struct ChunkArgs {
 
 __host__ __device__ inline int chunk_blocks(int n, int G) { return (n + kChunkRows / G - 1) / (kChunkRows / G); }
 
+// The steps of warpgroup q in an item: `total` half tiles of 64 keys from the item's first on, cut off where
+// the last row of its query tile sees no further; of a paired item those of the tiles i with i % 2 == q.
+struct ChunkSteps {
+    int total;
+    __device__ __forceinline__ ChunkSteps(const ChunkEntry &e, int q, int G, int causal) {
+        const int r1 = e.pair ? e.ntok * G : min(128 * q + 128, e.ntok * G);
+        const int see = min(e.len, causal ? e.first + (r1 - 1) / G : e.len);
+        const bool rows = e.pair || r1 > 128 * q;
+        total = rows ? max(0, min(see, e.kt1 * 128) - e.kt0 * 128 + 63) / 64 : 0;
+    }
+    // half tiles of tile i
+    __device__ __forceinline__ int of(int i) const { return max(0, min(2, total - 2 * i)); }
+};
+
 // ---------------------------------------------------------------------------------
 // The plan.
 // ---------------------------------------------------------------------------------
 // Costs in units of one key tile of an item: what a further item costs its CTA (filling and draining
 // the pipeline, the result), and what the merge of a split adds at the end.
 constexpr int kChunkItemCost = 2;
-constexpr int kChunkMergeCost = 2;
+constexpr int kChunkMergeCost = 2, kChunkMergeRows = 4;  // a merge: the first, and the second for a full block
+constexpr int kChunkPlanSeqs = 512, kChunkPlanBlocks = 2048;  // what the plan keeps in shared memory, at most
 constexpr int kChunkSortBins = 1024;
 
 __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const ChunkArgs a) {
     constexpr unsigned FULL = 0xffffffffu;
     __shared__ int sh_bad, sh_last, sh_scan[kChunkPlanThreads / 32], sh_run;
     __shared__ int hist[kChunkSortBins];
+    __shared__ ChunkSeq sh_seqs[kChunkPlanSeqs];
+    __shared__ int sh_base[kChunkPlanSeqs + 1], sh_tiles[kChunkPlanBlocks];
     __shared__ long long est[8];
     __shared__ int est_chunk[8];
     __shared__ long long sh_sum;
@@ -157,9 +175,16 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
     if (!sh_last) return;
     __threadfence();
 
+    // small plans are worked out in shared memory, larger ones in the workspace
+    const ChunkSeq *seqs = a.batch <= kChunkPlanSeqs ? sh_seqs : a.seqs;
+    int *base = a.batch <= kChunkPlanSeqs ? sh_base : a.base;
     // blocks before each sequence; a bad range refuses every sequence (the ranges may overlap)
     bool range_ok = true;
-    for (int s = tid; s < a.batch; s += kChunkPlanThreads) range_ok = range_ok && __ldcg(&a.seqs[s].bad) != kDevBadRange;
+    for (int s = tid; s < a.batch; s += kChunkPlanThreads) {
+        const int4 v = __ldcg(reinterpret_cast<const int4 *>(a.seqs + s));
+        if (a.batch <= kChunkPlanSeqs) sh_seqs[s] = ChunkSeq{v.x, v.y, v.z, v.w};
+        range_ok = range_ok && v.w != kDevBadRange;
+    }
     range_ok = __syncthreads_and(range_ok);
     if (tid == 0) {
         sh_run = 0;
@@ -172,7 +197,7 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
     for (int c0 = 0; c0 < a.batch; c0 += kChunkPlanThreads) {
         const int s = c0 + tid;
         int nb = 0;
-        if (range_ok && s < a.batch && __ldcg(&a.seqs[s].bad) == 0) nb = chunk_blocks(__ldcg(&a.seqs[s].n), G);
+        if (range_ok && s < a.batch && seqs[s].bad == 0) nb = chunk_blocks(seqs[s].n, G);
         int inc = nb;
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(FULL, inc, o);
@@ -182,13 +207,13 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
         __syncthreads();
         int before = sh_run;
         for (int w = 0; w < warp; ++w) before += sh_scan[w];
-        if (s < a.batch) a.base[s] = before + inc - nb;
+        if (s < a.batch) base[s] = before + inc - nb;
         __syncthreads();
         if (tid == kChunkPlanThreads - 1) sh_run = before + inc;
         __syncthreads();
     }
     const int n_blocks = sh_run;
-    if (tid == 0) a.base[a.batch] = n_blocks;
+    int *tiles = n_blocks <= kChunkPlanBlocks ? sh_tiles : a.tiles;
     __syncthreads();
     const int LH = a.n_layers * a.n_kv;
     // sequence of block e, and its line without splits
@@ -196,13 +221,13 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
         int lo = 0, hi = a.batch;  // the last s with base[s] <= e: empty sequences before it are skipped
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (a.base[mid] <= e) lo = mid; else hi = mid;
+            if (base[mid] <= e) lo = mid; else hi = mid;
         }
-        const int n = __ldcg(&a.seqs[lo].n), len = __ldcg(&a.seqs[lo].len);
-        const int b = e - a.base[lo];
+        const int n = seqs[lo].n, len = seqs[lo].len;
+        const int b = e - base[lo];
         ChunkEntry x;
         x.s = lo;
-        x.tok0 = __ldcg(&a.seqs[lo].q0) + b * tpb;
+        x.tok0 = seqs[lo].q0 + b * tpb;
         x.ntok = min(tpb, n - b * tpb);
         x.len = len;
         x.first = a.causal ? len - n + b * tpb + 1 : len;
@@ -213,7 +238,7 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
         x.split = 0;
         x.slot = 0;
         x.group = 0;
-        x.pad = 0;
+        x.pair = 0;
         return x;
     };
     {
@@ -221,7 +246,7 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
         int mx = 0;
         for (int e = tid; e < n_blocks; e += kChunkPlanThreads) {
             const ChunkEntry x = block_of(e);
-            a.tiles[e] = x.kt1;
+            tiles[e] = x.kt1;
             sum += x.kt1;
             mx = max(mx, x.kt1);
         }
@@ -245,9 +270,9 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
         const long long want = (even * num[warp] + den[warp] - 1) / den[warp];
         const int chunk = warp == 0 ? max(1, sh_max) : (int)max(2LL, min((long long)max(1, sh_max), want));
         long long items = 0, work = 0;
-        int longest = 0, slots = 0, lines = 0;
+        int longest = 0, slots = 0, lines = 0, merge_rows = 0;
         for (int e = lane; e < n_blocks; e += 32) {
-            const int t = a.tiles[e];
+            const int t = tiles[e];
             int ns = max(1, (t + chunk - 1) / chunk);
             const int per = (t + ns - 1) / ns;
             if (t > 0) ns = (t + per - 1) / per;
@@ -255,7 +280,10 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
             lines += ns;
             work += t + (long long)ns * kChunkItemCost;
             longest = max(longest, per);
-            if (ns > 1) slots += ns;
+            if (ns > 1) {
+                slots += ns;
+                merge_rows = max(merge_rows, min(tpb, a.n_tokens));
+            }
         }
         for (int o = 16; o; o >>= 1) {
             items += __shfl_xor_sync(FULL, items, o);
@@ -268,7 +296,7 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
             const long long rounds = (items * LH + a.sm_count - 1) / a.sm_count;
             const long long one = longest + kChunkItemCost;
             long long cost = min(rounds * one, (work * LH + a.sm_count - 1) / a.sm_count + one);
-            if (slots > 0) cost += kChunkMergeCost;
+            if (slots > 0) cost += kChunkMergeCost + kChunkMergeRows * merge_rows / tpb;
             if ((long long)slots * LH > a.max_slots || lines > a.max_entries) cost = 1LL << 60;
             est[warp] = cost;
             est_chunk[warp] = chunk;
@@ -289,11 +317,10 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
     const int chunk = sh_chunk;
     auto bin_of = [](int per) { return kChunkSortBins - 1 - min(per, kChunkSortBins - 1); };
     for (int e = tid; e < n_blocks; e += kChunkPlanThreads) {
-        const int t = a.tiles[e];
+        const int t = tiles[e];
         int ns = max(1, (t + chunk - 1) / chunk);
         const int per = (t + ns - 1) / ns;
         if (t > 0) ns = (t + per - 1) / per;
-        a.per[e] = per;
         atomicAdd(&hist[bin_of(per)], ns);
     }
     __syncthreads();
@@ -314,8 +341,10 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
     __syncthreads();
     for (int e = tid; e < n_blocks; e += kChunkPlanThreads) {
         ChunkEntry x = block_of(e);
-        const int t = x.kt1, per = a.per[e];
-        const int ns = t > 0 ? (t + per - 1) / per : 1;
+        const int t = x.kt1;
+        int ns = max(1, (t + chunk - 1) / chunk);
+        const int per = (t + ns - 1) / ns;
+        if (t > 0) ns = (t + per - 1) / per;
         const int at = atomicAdd(&hist[bin_of(per)], ns);
         x.nsplit = ns;
         if (ns > 1) {
@@ -326,6 +355,7 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
             x.split = k;
             x.kt0 = k * per;
             x.kt1 = min(t, (k + 1) * per);
+            x.pair = x.ntok * G <= 128 && x.kt1 - x.kt0 >= 2;
             a.entries[at + k] = x;
         }
     }
@@ -368,6 +398,32 @@ __device__ __forceinline__ void chunk_mma_ss(uint32_t d_tmem, uint32_t a_low, ui
         "r"(a_low), "r"(b_low), "r"(idesc), "r"(acc), "r"(kDescHigh)
         : "memory");
 }
+// One thread of a converged warp, in the form from which the compiler knows that the code under it runs
+// once and keeps the operands of the MMAs in uniform registers (under a plain lane test it moved each
+// operand of each MMA over by itself: 94 clocks an MMA against 64 of the tensor core).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// Three-input maximum that keeps a NaN.
+__device__ __forceinline__ float max3nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// A position in the ring of tiles.
+template <int NST>
+struct ChunkRing {
+    int stage = 0;
+    unsigned phase = 0;
+    __device__ __forceinline__ void step() {
+        if (++stage == NST) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+};
 // A (bf16 pairs, one row per lane) in tensor memory.
 __device__ __forceinline__ void chunk_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, int acc) {
     asm volatile(
@@ -392,6 +448,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15};" ::TRI_U8(r, 0),
+        TRI_U8(r, 8), "r"(taddr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -408,17 +471,42 @@ __device__ __forceinline__ void tmem_after32(uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 2^x of a pair on the FMA pipe: x = n + f with |f| <= 1/2 (round to nearest by adding 1.5 * 2^23, the
+// reduction of Cody and Waite), 2^f by the degree-4 polynomial of least largest relative error on
+// [-1/2, 1/2] (2.6e-6, found by Remez exchange), n added to the exponent. x <= 127. Below -126, at -infinity
+// and for a NaN: about 2^-126, which weighs nothing beside a row's largest weight (2^-8 at least); a row
+// that sees no key, or a NaN, is told by its maximum.
+__device__ __forceinline__ float2 exp2_pair(float2 x) {
+    x.x = fmaxf(x.x, -126.f);
+    x.y = fmaxf(x.y, -126.f);
+    const float2 magic = make_float2(12582912.f, 12582912.f), unmagic = make_float2(-12582912.f, -12582912.f);
+    const float2 t = __fadd2_rn(x, magic);
+    const float2 n = __fadd2_rn(t, unmagic);
+    const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
+    float2 p = __ffma2_rn(f, make_float2(0.009570102207362652f, 0.009570102207362652f),
+                          make_float2(0.05591785907745361f, 0.05591785907745361f));
+    p = __ffma2_rn(p, f, make_float2(0.240247443318367f, 0.240247443318367f));
+    p = __ffma2_rn(p, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
+    p = __ffma2_rn(p, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
+    return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
+                       __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+}
+
+constexpr int kChunkEmu128 = 1, kChunkEmu64 = 2;
+
 struct ChunkSmem {
-    unsigned q, ring, bars, total;
+    unsigned q, ring, ml, bars, total;
 };
-__host__ __device__ inline ChunkSmem chunk_smem(int D, int nst) {
+__host__ __device__ inline ChunkSmem chunk_smem(int D) {
     ChunkSmem L;
+    const unsigned NST = (unsigned)chunk_stages(D);
     L.q = 0;
     L.ring = 2u * (unsigned)D * 256u;               // two query tiles of 128 rows
-    L.bars = L.ring + (unsigned)nst * (unsigned)D * 256u;
-    // full[nst], empty[nst], q full and empty, S, P and O full [2 each], done, parts written and merge
-    // decided [2 each], TMEM address, abort, merge[2]
-    L.total = L.bars + (2u * kChunkMaxStages + 13u) * 8u + 32u + 1024u;  // + alignment slack
+    L.ml = L.ring + NST * (unsigned)D * 256u;  // a paired item's second (m, l) of each row
+    L.bars = L.ml + 128u * 8u;
+    // full, empty [stages each], q full and empty, S and P full [4 each: warpgroup, half], P V and O done [2 each], done, parts written and merge
+    // decided [2 each], exchange full and free, TMEM address, abort, merge[2]
+    L.total = L.bars + (2u * NST + 21u) * 8u + 32u + 1024u;  // + alignment slack
     return L;
 }
 
@@ -464,6 +552,149 @@ __device__ __forceinline__ void chunk_row_again(const ChunkArgs &a, int s, int l
     }
 }
 
+// A step of one row, 64 keys: S from tensor memory, masked, into the running (m, l); P over S. `left`: the
+// step's keys that the row sees (cut: some row of the tile sees fewer than 64). `fresh`: the row's first step.
+// pv: completes a phase with every P V of the warpgroup, pv_parity that of the last step's (of which at most
+// that one is outstanding: this step's S followed the one before it).
+//
+// The hardware exponential takes 8 clocks a warp, 512 for the step; `kEmu` of every 8 pairs are evaluated on the
+// FMA pipe instead.
+template <int D>
+__device__ __forceinline__ bool chunk_softmax_step(uint32_t ts, uint32_t to, float c, bool cut, int left, bool fresh,
+                                                   float &m, float &l, uint64_t *pv, unsigned pv_parity, int tries) {
+    constexpr unsigned FULL = 0xffffffffu;
+    constexpr int kEmu = D == 128 ? kChunkEmu128 : kChunkEmu64;
+    const float NEG_INF = __int_as_float(0xff800000);
+    uint32_t s0[32], s1[32];
+    float x0 = NEG_INF, x1 = NEG_INF, x2 = NEG_INF, x3 = NEG_INF;
+    auto top = [&](uint32_t(&s)[32], int at) {
+        if (cut) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (at + j >= left) s[j] = 0xff800000u;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+            x0 = max3nan(x0, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+            x1 = max3nan(x1, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+            x2 = max3nan(x2, __uint_as_float(s[j + 4]), __uint_as_float(s[j + 5]));
+            x3 = max3nan(x3, __uint_as_float(s[j + 6]), __uint_as_float(s[j + 7]));
+        }
+    };
+    tmem_ld32(ts, s0);
+    tmem_ld32(ts + 32u, s1);
+    tmem_wait32(s0);
+    tmem_after32(s1);
+    top(s0, 0);
+    top(s1, 32);
+    const float mx = max3nan(max3nan(x0, x1, x2), x3, x3);
+    if (fresh) {
+        m = mx;
+    } else if (__any_sync(FULL, mx != NEG_INF && !((mx - m) * c <= 8.f))) {
+        // once P V of the step before is complete, O is this warpgroup's to rescale
+        if (!__all_sync(FULL, mbar_wait_bounded(pv, pv_parity, tries))) return false;
+        tc_fence_after();
+        const float mn = max3nan(m, mx, mx);
+        const float f = m == mn ? 1.f : ex2_approx((m - mn) * c);
+        m = mn;
+        l *= f;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 16) {
+            uint32_t o[16];
+            tmem_ld16_issue(to + c0, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st16(to + c0, o);
+        }
+    }
+    // a NaN logit, or an infinite one (inf - inf), makes the row's maximum NaN and with it all its weights
+    const float mc = m == NEG_INF ? 0.f : (m + (m - m)) * c;
+    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+    const float2 c2 = make_float2(c, c), m2 = make_float2(-mc, -mc);
+    uint32_t p[32];
+    auto weights = [&](const uint32_t(&s)[32], int at) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            float2 y = __ffma2_rn(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), c2, m2);
+            if (j / 2 * kEmu % 8 + kEmu > 7 && kEmu > 0)
+                y = exp2_pair(y);
+            else
+                y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            if (j % 4 == 0) sum0 = __fadd2_rn(sum0, y); else sum1 = __fadd2_rn(sum1, y);
+            p[at + j / 2] = pack_bf16(y.x, y.y);
+        }
+    };
+    weights(s0, 0);
+    weights(s1, 16);
+    tmem_st32(ts, p);
+    l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+    tmem_wait_st();
+    return true;
+}
+
+// Join the parts of a block's row tile in the order of the keys: `first` + 2 k for k < nsplit. Each thread
+// takes one row (of the rows rounded up to a power of two) and every (128 / rows)-th piece of 4 dims, 4 pieces
+// of 4 parts in flight.
+template <int D>
+__device__ __forceinline__ void chunk_merge(const ChunkArgs &a, long long first, int nsplit, int nv, int t, int G, int r0,
+                                            int lr, int g, int tok0) {
+    const float NEG_INF = __int_as_float(0xff800000);
+    const int shift = 32 - __clz(nv - 1);       // nv >= 1: rows rounded up to 2^shift
+    const int rr = t & ((1 << shift) - 1), step = 128 >> shift;
+    if (rr >= nv) return;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + first * 128 + rr;
+    float M = NEG_INF;
+#pragma unroll 4
+    for (int k = 0; k < nsplit; ++k) M = fmaxf(M, __ldcg(ml + k * 256).x);
+    float L = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < nsplit; ++k) {
+        const float2 x = __ldcg(ml + k * 256);
+        if (x.y != 0.f) L += x.y * ex2_approx(x.x - M);  // a part that sees no key of the row weighs nothing
+    }
+    const float li = L == 0.f ? 0.f : 1.f / L;
+    const int row = r0 + rr, rh = g * G + row % G;
+    const long long tok = tok0 + row / G;
+    const float4 *part = reinterpret_cast<const float4 *>(a.part) + (first * (D / 4)) * 128 + rr;
+    uint16_t *out = a.out + lr * a.o_l + tok * a.o_t + rh * a.o_h;
+    for (int c0 = t >> shift; c0 < D / 4; c0 += 4 * step) {
+        float4 A[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) A[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < nsplit; ++k) {
+            const float2 x = __ldcg(ml + k * 256);
+            const float w = x.y == 0.f ? 0.f : ex2_approx(x.x - M);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = c0 + i * step;
+                if (c < D / 4) {
+                    const float4 v = __ldcg(part + ((long long)k * 2 * (D / 4) + c) * 128);
+                    if (x.y != 0.f) {
+                        A[i].x = fmaf(v.x, w, A[i].x);
+                        A[i].y = fmaf(v.y, w, A[i].y);
+                        A[i].z = fmaf(v.z, w, A[i].z);
+                        A[i].w = fmaf(v.w, w, A[i].w);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = c0 + i * step;
+            if (c < D / 4) {
+                uint2 w;
+                w.x = pack_bf16(A[i].x * li, A[i].y * li);
+                w.y = pack_bf16(A[i].z * li, A[i].w * li);
+                *reinterpret_cast<uint2 *>(out + 4 * c) = w;
+            }
+        }
+    }
+    if (a.lse && t < (1 << shift))
+        a.lse[((long long)lr * a.n_tokens + tok) * (a.n_kv * G) + rh] = L == 0.f ? NEG_INF : (M + log2f(L)) * 0.6931471805599453f;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     tri_chunk_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -476,38 +707,47 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     extern __shared__ unsigned char chunk_smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(chunk_smem_raw) + 1023) &
                                                             ~uintptr_t(1023));
-    const int nst = a.nst;
-    const ChunkSmem Ly = chunk_smem(D, nst);
+    constexpr int NST = chunk_stages(D);
+    const ChunkSmem Ly = chunk_smem(D);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Ly.bars);
-    uint64_t *empty = full + kChunkMaxStages;
-    uint64_t *qfull = empty + kChunkMaxStages;
+    uint64_t *empty = full + NST;
+    uint64_t *qfull = empty + NST;
     uint64_t *qempty = qfull + 1;
-    uint64_t *sfull = qempty + 1;   // [2]
-    uint64_t *pfull = sfull + 2;    // [2]
-    uint64_t *ofull = pfull + 2;    // [2]
+    uint64_t *sfull = qempty + 1;   // [warpgroup][half]
+    uint64_t *pfull = sfull + 4;    // [warpgroup][half]
+    uint64_t *pv = pfull + 4;       // [warpgroup]
+    uint64_t *ofull = pv + 2;       // [warpgroup]
     uint64_t *done = ofull + 2;
     uint64_t *parts = done + 1;     // [2]
     uint64_t *decided = parts + 2;  // [2]
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(decided + 2);
+    uint64_t *xfull = decided + 2;
+    uint64_t *xfree = xfull + 1;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(xfree + 1);
+    float2 *ml_x = reinterpret_cast<float2 *>(smem + Ly.ml);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     volatile int *merge_flag = abort_flag + 1;        // [2]
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
-        for (int i = 0; i < nst; ++i) {
+        for (int i = 0; i < NST; ++i) {
             mbar_init(full + i, 1);
-            mbar_init(empty + i, 1);
+            mbar_init(empty + i, 2);
         }
         mbar_init(qfull, 1);
-        mbar_init(qempty, 1);
-        for (int i = 0; i < 2; ++i) {
+        mbar_init(qempty, 2);        // an arrival of each MMA warp
+        for (int i = 0; i < 4; ++i) {
             mbar_init(sfull + i, 1);
             mbar_init(pfull + i, 4);  // the warpgroup's warps
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(pv + i, 1);
             mbar_init(ofull + i, 1);
             mbar_init(parts + i, 4);
             mbar_init(decided + i, 1);
         }
-        mbar_init(done, 1);
+        mbar_init(done, 2);
+        mbar_init(xfull, 4);
+        mbar_init(xfree, 4);
         *abort_flag = 0;
         mbar_init_fence();
     }
@@ -540,6 +780,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChunkRegsFew));
     if (warp == 0) {
         // ---------------- loads ----------------
+        ChunkRing<NST> fill;
         int k = 0, nq = 0;      // ring fills so far, query tiles loaded so far
         bool ok = true;
         for (int r = 0; ok && !*abort_flag; ++r) {
@@ -566,96 +807,139 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const bool withhold = e.kt0 == 0 && ((long long)lr * a.batch + e.s) * a.n_kv + g == a.inject_unit;
             auto page_of = [&](int kt) {
                 const int r0 = kt * 128 + p * pr;
-                return (a.paged && p < np && r0 < e.len)
+                return (a.paged && p < np && r0 < e.len && kt < e.kt1)
                            ? __ldg(a.block_table + (long long)e.s * a.max_pages + r0 / a.page_size) : 0;
             };
-            int page = page_of(e.kt0);
-            for (int kt = e.kt0; kt < e.kt1 && ok; ++kt) {
+            // tiles in the order in which the MMA warp takes them: the first key tile (two of a paired
+            // item), then each value tile followed by the key tile `lead` after it
+            const int lead = e.pair ? 2 : 1, n = e.kt1 - e.kt0;
+            int pages[3] = {page_of(e.kt0), page_of(e.kt0 + 1), page_of(e.kt0 + 2)};  // of the next value tile on
+            auto tile = [&](int kt, int page, const CUtensorMap *map, bool skip) {
                 const int r0 = kt * 128 + p * pr;
-                const bool mine = p < np && r0 < e.len;
                 long long row;
                 if (a.paged)
                     row = (((long long)lr * a.n_pages + page) * a.n_kv + g) * (long long)a.page_size + r0 % a.page_size;
                 else
                     row = (((long long)lr * a.batch + e.s) * a.n_kv + g) * (long long)a.cap_u + r0;
-                if (kt + 1 < e.kt1) page = page_of(kt + 1);
                 const int pieces = min(np, (e.len - kt * 128 + pr - 1) / pr);
-                for (int kv = 0; kv < 2; ++kv, ++k) {
-                    const int st = k % nst;
-                    if (k >= nst &&
-                        !__all_sync(FULL, mbar_wait_bounded(empty + st, (unsigned)((k / nst - 1) & 1), a.wait_tries))) {
-                        if (lane == 0) fail(e, lh);
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) {
-                        // the MMA warp may have written zeros to this stage (generic proxy)
-                        fence_proxy_async_smem();
-                        mbar_expect_tx(full + st, (unsigned)(pieces * pr) * 128u * KCH);
-                    }
-                    __syncwarp();
-                    // test hook: the unit's first key tile is armed but never loaded
-                    if (mine && !(withhold && kt == 0 && kv == 0))
-                        tma_tile_2d(smem + Ly.ring + (unsigned)st * kTileBytes + c * kChunkBytes + (unsigned)(p * pr) * 128u,
-                                    kv ? &vmap : &kmap, c * 64, (int)row, full + st);
+                const int st = fill.stage;
+                if (k >= NST && !__all_sync(FULL, mbar_wait_bounded(empty + st, fill.phase ^ 1u, a.wait_tries))) {
+                    if (lane == 0) fail(e, lh);
+                    return false;
                 }
+                if (lane == 0) {
+                    // the MMA warp may have written zeros to this stage (generic proxy)
+                    fence_proxy_async_smem();
+                    mbar_expect_tx(full + st, (unsigned)(pieces * pr) * 128u * KCH);
+                }
+                __syncwarp();
+                if (p < np && r0 < e.len && !skip)
+                    tma_tile_2d(smem + Ly.ring + (unsigned)st * kTileBytes + c * kChunkBytes + (unsigned)(p * pr) * 128u, map,
+                                c * 64, (int)row, full + st);
+                ++k;
+                fill.step();
+                return true;
+            };
+            // test hook: the unit's first key tile is armed but never loaded
+            ok = tile(e.kt0, pages[0], &kmap, withhold);
+            if (ok && e.pair) ok = tile(e.kt0 + 1, pages[1], &kmap, false);
+            for (int i = 0; ok && i < n; ++i) {
+                const int next = page_of(e.kt0 + i + 3);
+                ok = tile(e.kt0 + i, pages[0], &vmap, false);
+                if (ok && i + lead < n) ok = tile(e.kt0 + i + lead, pages[lead], &kmap, false);
+                pages[0] = pages[1];
+                pages[1] = pages[2];
+                pages[2] = next;
             }
         }
         // copies still in flight must land before the CTA exits
-        for (int j = k > nst ? k - nst : 0; j < k; ++j)
-            (void)mbar_wait_bounded(full + j % nst, (unsigned)((j / nst) & 1), a.wait_tries);
+        for (int j = k > NST ? k - NST : 0; j < k; ++j)
+            (void)mbar_wait_bounded(full + j % NST, (unsigned)((j / NST) & 1), a.wait_tries);
         if (nq > 0) (void)mbar_wait_bounded(qfull, (unsigned)((nq - 1) & 1), a.wait_tries);
         __syncwarp();
-    } else if (warp == 1) {
-        // ---------------- MMAs ----------------
-        const uint32_t id_s = mx_idesc(128), id_o = mx_idesc(D) | (1u << 16);  // V is N-major
+    } else if (warp <= 2) {
+        // ---------------- MMAs: one warp for each warpgroup's, so that one's waits and bookkeeping run beside
+        // the other's MMAs
+        const int q = warp - 1;
+        const uint32_t id_s = mx_idesc(64), id_o = mx_idesc(D) | (1u << 16);  // V is N-major
         const uint32_t q_low = desc_low(smem_u32(smem + Ly.q), 16u), k_low = desc_low(smem_u32(smem + Ly.ring), 16u);
         const uint32_t v_low = desc_low(smem_u32(smem + Ly.ring), kChunkBytes);
-        int k = 0, nq = 0, np[2] = {0, 0};  // tiles consumed, items, P tiles taken
+        const uint32_t sd = tmem + 128u * q, od = tmem + 256u + (uint32_t)(D * q);
+        ChunkRing<NST> at;            // the next tile
+        unsigned nq = 0, np0 = 0, np1 = 0;  // items, P of each half so far
         bool ok = true;
         auto wait = [&](uint64_t *bar, unsigned phase) {
             return __all_sync(FULL, mbar_wait_bounded(bar, phase & 1u, a.wait_tries));
+        };
+        // a tile that this warp does not use: its release takes an arrival of each
+        auto skip = [&] {
+            ok = ok && wait(full + at.stage, at.phase);
+            if (ok && lane == 0) mbar_arrive(empty + at.stage);
+            at.step();
         };
         for (int r = 0; ok && !*abort_flag; ++r) {
             const long long it = item_of(r);
             if (it >= n_items) break;
             const ChunkEntry e = a.entries[it / LH];
-            const int lh = (int)(it % LH);
-            const int n = e.kt1 - e.kt0;
+            // (values that the compiler shall know to be the same in every lane go through a shuffle)
+            const int n = __shfl_sync(FULL, e.kt1 - e.kt0, 0);
             if (n <= 0) continue;
-            const int ntile = e.ntok * G > 128 ? 2 : 1;
-            auto mma_s = [&](int q, int st) {
-                const uint32_t al = q_low + q * (kTileBytes >> 4), bl = k_low + (unsigned)st * (kTileBytes >> 4);
+            const bool pair = __shfl_sync(FULL, e.pair, 0) != 0;
+            const int lead = pair ? 2 : 1, left = __shfl_sync(FULL, e.len - e.kt0 * 128, 0);
+            ChunkSteps steps(e, q, G, a.causal);
+            steps.total = __shfl_sync(FULL, steps.total, 0);
+            const uint32_t ql = q_low + (pair ? 0u : (uint32_t)q * (kTileBytes >> 4));
+            // S of 64 keys into its half of the warpgroup's columns
+            auto mma_s = [&](uint32_t bl, int h) {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const unsigned off = ((unsigned)(ks >> 2) * kChunkBytes + (unsigned)(ks & 3) * 32u) >> 4;
-                    chunk_mma_ss(tmem + 128u * q, al + off, bl + off, id_s, ks > 0);
+                    chunk_mma_ss(sd + 64u * h, ql + off, bl + h * 512u + off, id_s, ks > 0);
                 }
-                mx_commit(sfull + q);
+                mx_commit(sfull + 2 * q + h);
             };
-            ok = wait(qfull, nq) && wait(full + k % nst, k / nst);
-            if (!ok) {
-                if (lane == 0) fail(e, lh);
-                break;
-            }
+            auto mine = [&](int i) { return pair && (i & 1) != q ? 0 : steps.of(i); };
+            ok = wait(qfull, nq);
             ++nq;
-            tc_fence_after();
-            if (lane == 0) {
-                for (int q = 0; q < ntile; ++q) mma_s(q, k % nst);
-                mx_commit(empty + k % nst);
-                if (n == 1) mx_commit(qempty);
+            bool used = false;        // the query tile
+            for (int t = 0; ok && t < lead; ++t) {
+                const int hs = mine(t);
+                if (hs == 0) {
+                    skip();
+                    continue;
+                }
+                used = true;
+                ok = wait(full + at.stage, at.phase);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t bl = __shfl_sync(FULL, k_low + (unsigned)at.stage * (kTileBytes >> 4), 0);
+                if (elect_one()) {
+                    mma_s(bl, 0);
+                    if (hs > 1) mma_s(bl, 1);
+                    mx_commit(empty + at.stage);
+                    if (t + lead >= n || mine(t + lead) == 0) mx_commit(qempty);
+                }
+                __syncwarp();
+                at.step();
             }
-            __syncwarp();
-            ++k;
-            for (int i = 0; i < n && ok; ++i) {
-                const int sv = k % nst, sk = (k + 1) % nst;  // this tile's V, the next tile's K
-                ok = wait(full + sv, k / nst);
+            if (ok && !used && lane == 0) mbar_arrive(qempty);
+            for (int i = 0; ok && i < n; ++i) {
+                const bool more = i + lead < n;
+                const int hs = mine(i), hn = more ? mine(i + lead) : 0;
+                if (hs == 0) {
+                    skip();
+                    if (more) skip();
+                    continue;
+                }
+                const ChunkRing<NST> av = at;  // this tile's V; `at`: the K `lead` tiles on
+                at.step();
+                ok = wait(full + av.stage, av.phase);
                 if (!ok) break;
                 // value rows past the length hold whatever was there: zero them, for a zero weight does
-                // not clear a NaN
-                const int valid = e.len - (e.kt0 + i) * 128;
+                // not clear a NaN (both warps of a tile that they share write the same zeros)
+                const int valid = left - i * 128;
                 if (valid < 128) {
-                    unsigned char *Vs = smem + Ly.ring + (unsigned)sv * kTileBytes;
+                    unsigned char *Vs = smem + Ly.ring + (unsigned)av.stage * kTileBytes;
                     const int words = (128 - valid) * 8;  // 16-byte words of a chunk
                     for (int w = lane; w < words * KCH; w += 32) {
                         const int c = w / words, x = w % words;
@@ -665,40 +949,47 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                for (int q = 0; q < ntile; ++q) {
-                    ok = ok && wait(pfull + q, np[q]);
-                    if (!ok) break;
-                    ++np[q];
-                    if (i + 1 < n && q == 0) ok = wait(full + sk, (k + 1) / nst);
-                    if (!ok) break;
+                const uint32_t vl = __shfl_sync(FULL, v_low + (unsigned)av.stage * (kTileBytes >> 4), 0);
+                const uint32_t bl = __shfl_sync(FULL, k_low + (unsigned)at.stage * (kTileBytes >> 4), 0);
+                ok = !hn || wait(full + at.stage, at.phase);
+                if (!ok) break;
+                auto half = [&](int h, unsigned &np) {
+                    ok = wait(pfull + 2 * q + h, np);
+                    ++np;
+                    if (!ok) return;
                     tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t vl = v_low + (unsigned)sv * (kTileBytes >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)  // 16 keys: 16 rows of 128 bytes of each chunk
-                            chunk_mma_ts(tmem + 256u + (uint32_t)(D * q), tmem + 128u * q + 8u * ks, vl + ks * 128u, id_o,
-                                         (i > 0 || ks > 0));
-                        if (i + 1 < n) mma_s(q, sk);
-                        else mx_commit(ofull + q);
+                        for (int ks = 0; ks < 4; ++ks)  // 16 keys: 16 rows of 128 bytes of each chunk
+                            chunk_mma_ts(od, sd + 64u * h + 8u * ks, vl + (4 * h + ks) * 128u, id_o,
+                                         (i >= lead || h > 0 || ks > 0));
+                        mx_commit(pv + q);
+                        if (hn > h) mma_s(bl, h);
+                        if (h + 1 == hs) {
+                            mx_commit(empty + av.stage);
+                            if (!hn) {
+                                mx_commit(ofull + q);
+                            } else {
+                                mx_commit(empty + at.stage);
+                                if (i + 2 * lead >= n || mine(i + 2 * lead) == 0) mx_commit(qempty);
+                            }
+                        }
                     }
                     __syncwarp();
-                }
+                };
+                half(0, np0);
+                if (ok && hs > 1) half(1, np1);
                 if (!ok) break;
-                if (lane == 0) {
-                    mx_commit(empty + sv);
-                    if (i + 1 < n) mx_commit(empty + sk);
-                    if (i + 2 == n) mx_commit(qempty);
-                }
-                __syncwarp();
-                k += i + 1 < n ? 2 : 1;
+                if (hn) at.step();
+                else if (more) skip();
             }
             if (!ok) {
-                if (lane == 0) fail(e, lh);
+                if (lane == 0) fail(e, (int)(it % LH));
                 break;
             }
         }
         // MMAs may still run (after a wait that ran out): they must end before the TMEM is released
-        if (lane == 0) mx_commit(done);
+        if (elect_one()) mx_commit(done);
         __syncwarp();
         (void)mbar_wait_bounded(done, 0u, a.wait_tries);
         __syncwarp();
@@ -711,175 +1002,172 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + 128u * q, to = tmem + lanes + 256u + (uint32_t)(D * q);
         const int wg_tid = tid & 127;
-        unsigned ns = 0, no = 0, nm = 0;                  // S tiles, items, items in parts so far
+        unsigned ns0 = 0, ns1 = 0, no = 0, nm = 0, nx = 0;  // S of each half, items, items in parts, paired items so far
         bool ok = true;
         for (int r = 0; ok && !*abort_flag; ++r) {
             const long long it = item_of(r);
             if (it >= n_items) break;
-            const ChunkEntry e = a.entries[it / LH];
-            const int lh = (int)(it % LH), lr = lh / a.n_kv, g = lh % a.n_kv;
-            const int n = e.kt1 - e.kt0;
-            const int rows = e.ntok * G - 128 * q;        // rows of this tile
-            if (rows <= 0) continue;
-            const int tok = (128 * q + row) / G, hd = (128 * q + row) % G;
-            const bool mine = row < rows;
-            const int limit = min(e.len, a.causal ? e.first + tok : e.len);
-            const int sure = min(e.len, a.causal ? e.first + 128 * q / G : e.len);  // seen by every row
+            const ChunkEntry *ep = a.entries + it / LH;
+            const int lh = (int)(it % LH);
             float m = NEG_INF, l = 0.f;
-            for (int i = 0; i < n; ++i) {
-                ok = __all_sync(FULL, mbar_wait_bounded(sfull + q, ns & 1u, a.wait_tries));
-                if (!ok) break;
-                ++ns;
-                tc_fence_after();
-                uint32_t s0[32], s1[32], s2[32], s3[32];
-                tmem_ld32(ts, s0);
-                tmem_ld32(ts + 32u, s1);
-                tmem_ld32(ts + 64u, s2);
-                tmem_ld32(ts + 96u, s3);
-                tmem_wait32(s0);
-                tmem_after32(s1);
-                tmem_after32(s2);
-                tmem_after32(s3);
-                const int key0 = (e.kt0 + i) * 128;
-                if (key0 + 128 > sure) {
-                    const int left = limit - key0;        // columns that this row sees
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (j >= left) s0[j] = 0xff800000u;
-                        if (j + 32 >= left) s1[j] = 0xff800000u;
-                        if (j + 64 >= left) s2[j] = 0xff800000u;
-                        if (j + 96 >= left) s3[j] = 0xff800000u;
+            int n, rows, limit;
+            bool pair, any;                                   // any: the warpgroup had steps (O holds something)
+            {
+                const ChunkEntry e = *ep;
+                pair = e.pair;
+                n = e.kt1 - e.kt0;
+                rows = e.ntok * G - (pair ? 0 : 128 * q);     // rows of this warpgroup's tile
+                if (rows <= 0) continue;
+                const int r0 = pair ? 0 : 128 * q;
+                limit = min(e.len, a.causal ? e.first + (r0 + row) / G : e.len);
+                const int sure = min(e.len, a.causal ? e.first + r0 / G : e.len);  // seen by every row
+                const bool work = (warp & 3) * 32 < rows;     // a warp without rows only keeps the step
+                const ChunkSteps steps(e, q, G, a.causal);
+                const int step = pair ? 2 : 1;
+                bool fresh = true;
+                for (int i = pair ? q : 0; ok && i < n; i += step) {
+                    const int hs = steps.of(i);
+                    for (int h = 0; ok && h < hs; ++h) {
+                        ok = __all_sync(FULL, mbar_wait_bounded(sfull + 2 * q + h, (h ? ns1 : ns0) & 1u, a.wait_tries));
+                        if (!ok) break;
+                        if (work) {
+                            tc_fence_after();
+                            const int key0 = (e.kt0 + i) * 128 + 64 * h;
+                            ok = chunk_softmax_step<D>(ts + 64u * h, to, a.c, key0 + 64 > sure, limit - key0, fresh, m, l,
+                                                       pv + q, (ns0 + ns1 - 1u) & 1u, a.wait_tries);
+                            if (!ok) break;
+                            tc_fence_before();
+                        }
+                        if (h) ++ns1; else ++ns0;
+                        fresh = false;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(pfull + 2 * q + h);
                     }
                 }
-                float x0 = NEG_INF, x1 = NEG_INF, x2 = NEG_INF, x3 = NEG_INF;
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    x0 = max3f(x0, __uint_as_float(s0[j]), __uint_as_float(s0[j + 1]));
-                    x1 = max3f(x1, __uint_as_float(s1[j]), __uint_as_float(s1[j + 1]));
-                    x2 = max3f(x2, __uint_as_float(s2[j]), __uint_as_float(s2[j + 1]));
-                    x3 = max3f(x3, __uint_as_float(s3[j]), __uint_as_float(s3[j + 1]));
+                any = !fresh;
+                if (ok && any) {
+                    ok = __all_sync(FULL, mbar_wait_bounded(ofull + q, no & 1u, a.wait_tries));
+                    ++no;
+                    tc_fence_after();
                 }
-                const float mx = fmaxf(max3f(x0, x1, x2), x3);
-                if (i == 0) {
-                    m = mx;
-                } else if (__any_sync(FULL, (mx - m) * a.c > 8.f)) {
-                    // P V of the tiles before is complete: O is this warpgroup's to rescale
-                    const float mn = fmaxf(m, mx);
-                    const float f = m == mn ? 1.f : ex2_approx((m - mn) * a.c);
-                    m = mn;
-                    l *= f;
-#pragma unroll
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(to + c0, o);
-                        tmem_wait32(o);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tmem_st32(to + c0, o);
-                    }
-                }
-                const float mc = m == NEG_INF ? 0.f : m * a.c;
-                float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-                auto weights = [&](const uint32_t(&s)[32], uint32_t *p) {
-                    const float2 c2 = make_float2(a.c, a.c), m2 = make_float2(-mc, -mc);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        float2 y0 = __ffma2_rn(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), c2, m2);
-                        float2 y1 = __ffma2_rn(make_float2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), c2, m2);
-                        y0 = make_float2(ex2_approx(y0.x), ex2_approx(y0.y));
-                        y1 = make_float2(ex2_approx(y1.x), ex2_approx(y1.y));
-                        sum0 = __fadd2_rn(sum0, y0);
-                        sum1 = __fadd2_rn(sum1, y1);
-                        p[j / 2] = pack_bf16(y0.x, y0.y);
-                        p[j / 2 + 1] = pack_bf16(y1.x, y1.y);
-                    }
-                };
-                uint32_t p[32];
-                weights(s0, p);
-                weights(s1, p + 16);
-                tmem_st32(ts, p);
-                weights(s2, p);
-                weights(s3, p + 16);
-                tmem_st32(ts + 32u, p);
-                l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(pfull + q);
-            }
-            if (!ok) {
-                if (lane == 0) fail(e, lh);
-                break;
-            }
-            if (n > 0) {
-                ok = __all_sync(FULL, mbar_wait_bounded(ofull + q, no & 1u, a.wait_tries));
                 if (!ok) {
                     if (lane == 0) fail(e, lh);
                     break;
                 }
-                ++no;
-                tc_fence_after();
             }
             // ---- the result of the item, or its part ----
-            const long long trow = e.tok0 + tok;
+            const int4 *e4 = reinterpret_cast<const int4 *>(ep);
+            const int4 ea = __ldcg(e4), eb = __ldcg(e4 + 1), ec = __ldcg(e4 + 2);
+            const int len = ea.w, kt0 = eb.y, kt1 = eb.z, nsplit = ec.x;
+            float w0 = 1.f, w1 = 0.f;
+            if (m == NEG_INF) l = 0.f;                        // no key: what is left of its zero weights goes
+            m *= a.c;                                         // the log2 domain (-inf stays)
+            if (pair) {
+                // the second warpgroup hands its rows' (m, l) over and its O, in the tensor memory lanes of the
+                // same rows, which the first joins to its own
+                if (q == 1) {
+                    ml_x[row] = make_float2(m, l);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(xfull);
+                    ok = __all_sync(FULL, mbar_wait_bounded(xfree, nx & 1u, a.wait_tries));
+                    ++nx;
+                    if (ok) continue;
+                } else {
+                    ok = __all_sync(FULL, mbar_wait_bounded(xfull, nx & 1u, a.wait_tries));
+                    ++nx;
+                    tc_fence_after();
+                    const float2 o = ml_x[row];
+                    const float M = fmaxf(m, o.x);
+                    w0 = l == 0.f ? 0.f : ex2_approx(m - M);
+                    w1 = o.y == 0.f ? 0.f : ex2_approx(o.x - M);
+                    l = (l == 0.f ? 0.f : l * w0) + (o.y == 0.f ? 0.f : o.y * w1);
+                    m = M;
+                }
+                if (!ok) {
+                    if (lane == 0) fail(*ep, lh);
+                    break;
+                }
+            }
+            const int r0 = pair ? 0 : 128 * q;
+            const int lr = lh / a.n_kv, g = lh % a.n_kv;
+            const int tok = (r0 + row) / G, hd = (r0 + row) % G;
+            const bool mine = row < rows;
+            const long long trow = ea.y + tok;
             const int head = g * G + hd;
             uint16_t *orow = a.out + lr * a.o_l + trow * a.o_t + head * a.o_h;
-            const long long slot = ((long long)e.slot * LH + (long long)lh * e.nsplit + e.split) * 2 + q;
+            const int tile = pair ? 0 : q;
+            const long long slot = ((long long)ec.z * LH + (long long)lh * nsplit + ec.y) * 2 + tile;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            float lse = NEG_INF;
-            if (l != 0.f) lse = (m * a.c + log2f(l)) * 0.6931471805599453f;
             bool odd = false;
+            if ((warp & 3) * 32 < rows) {
 #pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-                uint32_t o[32];
-                if (n > 0) {
-                    tmem_ld32(to + c0, o);
-                    tmem_wait32(o);
-                } else {
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    if (any) {
+                        tmem_ld32(to + c0, o);
+                        tmem_wait32(o);
+                        if (pair) {
+                            uint32_t o1[32];
+                            tmem_ld32(to + D + c0, o1);
+                            tmem_wait32(o1);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = 0u;
-                }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) odd |= (o[j] & 0x7f800000u) == 0x7f800000u;
-                if (e.nsplit == 1) {
-                    if (mine) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            uint4 w;
-                            w.x = pack_bf16(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
-                            w.y = pack_bf16(__uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
-                            w.z = pack_bf16(__uint_as_float(o[j + 4]) * inv, __uint_as_float(o[j + 5]) * inv);
-                            w.w = pack_bf16(__uint_as_float(o[j + 6]) * inv, __uint_as_float(o[j + 7]) * inv);
-                            *reinterpret_cast<uint4 *>(orow + c0 + j) = w;
+                            for (int j = 0; j < 32; ++j) {
+                                const float x = w0 == 0.f ? 0.f : __uint_as_float(o[j]) * w0;
+                                o[j] = __float_as_uint(w1 == 0.f ? x : fmaf(__uint_as_float(o1[j]), w1, x));
+                            }
                         }
-                    }
-                } else if (mine) {
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        *reinterpret_cast<float4 *>(a.part + ((slot * (D / 4) + (c0 + j) / 4) * 128 + row) * 4) =
-                            make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]), __uint_as_float(o[j + 2]),
-                                        __uint_as_float(o[j + 3]));
+                        for (int j = 0; j < 32; ++j) o[j] = 0u;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) odd |= (o[j] & 0x7f800000u) == 0x7f800000u;
+                    if (nsplit == 1) {
+                        if (mine) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8) {
+                                uint4 w;
+                                w.x = pack_bf16(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
+                                w.y = pack_bf16(__uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+                                w.z = pack_bf16(__uint_as_float(o[j + 4]) * inv, __uint_as_float(o[j + 5]) * inv);
+                                w.w = pack_bf16(__uint_as_float(o[j + 6]) * inv, __uint_as_float(o[j + 7]) * inv);
+                                *reinterpret_cast<uint4 *>(orow + c0 + j) = w;
+                            }
+                        }
+                    } else if (mine) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<float4 *>(a.part + ((slot * (D / 4) + (c0 + j) / 4) * 128 + row) * 4) =
+                                make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]), __uint_as_float(o[j + 2]),
+                                            __uint_as_float(o[j + 3]));
+                    }
                 }
             }
             tc_fence_before();
-            if (mine) {
-                if (e.nsplit > 1)
-                    *reinterpret_cast<float2 *>(a.part_ml + (slot * 128 + row) * 2) = make_float2(m * a.c, l);
-                else if (a.lse)
-                    a.lse[((long long)lr * a.n_tokens + trow) * (a.n_kv * G) + head] = lse;
+            if (pair) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(xfree);
             }
-            unsigned again = __ballot_sync(FULL, mine && odd && limit < min(e.len, e.kt1 * 128));
+            if (mine) {
+                if (nsplit > 1)
+                    *reinterpret_cast<float2 *>(a.part_ml + (slot * 128 + row) * 2) = make_float2(m, l);
+                else if (a.lse)
+                    a.lse[((long long)lr * a.n_tokens + trow) * (a.n_kv * G) + head] =
+                        l == 0.f ? NEG_INF : (m + log2f(l)) * 0.6931471805599453f;
+            }
+            unsigned again = __ballot_sync(FULL, mine && odd && limit < min(len, kt1 * 128));
             __syncwarp();
             while (again) {  // see chunk_row_again
                 const int src = __ffs(again) - 1;
                 again &= again - 1;
                 const int rt = __shfl_sync(FULL, tok, src), rh = __shfl_sync(FULL, hd, src), rl = __shfl_sync(FULL, limit, src);
                 float acc[D / 32], rm, rs;
-                chunk_row_again<D>(a, e.s, lr, g, a.q + lr * a.q_l + (e.tok0 + rt) * a.q_t + (g * G + rh) * a.q_h,
-                                   e.kt0 * 128, min(rl, e.kt1 * 128), acc, rm, rs);
+                chunk_row_again<D>(a, ea.x, lr, g, a.q + lr * a.q_l + (ea.y + rt) * a.q_t + (g * G + rh) * a.q_h,
+                                   kt0 * 128, min(rl, kt1 * 128), acc, rm, rs);
                 const int rr = (warp & 3) * 32 + src;
-                if (e.nsplit == 1) {
-                    uint16_t *dst = a.out + lr * a.o_l + (e.tok0 + rt) * a.o_t + (g * G + rh) * a.o_h;
+                if (nsplit == 1) {
+                    uint16_t *dst = a.out + lr * a.o_l + (ea.y + rt) * a.o_t + (g * G + rh) * a.o_h;
                     const float ri = rs == 0.f ? 0.f : 1.f / rs;
 #pragma unroll
                     for (int x = 0; x < D / 32; ++x)
@@ -894,61 +1182,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 __syncwarp();
             }
-            if (e.nsplit > 1) {
+            if (nsplit > 1) {
                 // the last part of the block to arrive merges them all, in the order of the keys
                 __threadfence();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(parts + q);
                 ok = __all_sync(FULL, mbar_wait_bounded(parts + q, nm & 1u, a.wait_tries));
                 if (ok && wg_tid == 0) {
-                    const long long grp = ((long long)e.group * LH + lh) * 2 + q;
-                    merge_flag[q] = atomicAdd(a.counters + grp, 1u) == (unsigned)e.nsplit - 1;
+                    const long long grp = ((long long)ec.w * LH + lh) * 2 + tile;
+                    merge_flag[q] = atomicAdd(a.counters + grp, 1u) == (unsigned)nsplit - 1;
                     __threadfence();
                     mbar_arrive(decided + q);
                 }
                 __syncwarp();
                 ok = ok && __all_sync(FULL, mbar_wait_bounded(decided + q, nm & 1u, a.wait_tries));
                 if (!ok) {
-                    if (lane == 0) fail(e, lh);
+                    if (lane == 0) fail(*ep, lh);
                     break;
                 }
                 ++nm;
                 // the flag is written again only after every warp has arrived with its next part
                 if (merge_flag[q]) {
-                    const long long first = ((long long)e.slot * LH + (long long)lh * e.nsplit) * 2 + q;
-                    const int nv = min(128, rows);
-                    for (int x = wg_tid; x < nv * (D / 4); x += 128) {
-                        const int rr = x % nv, c4 = x / nv;
-                        float M = NEG_INF;
-                        for (int k = 0; k < e.nsplit; ++k) {
-                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + ((first + 2 * k) * 128 + rr) * 2));
-                            M = fmaxf(M, ml.x);
-                        }
-                        float L = 0.f;
-                        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int k = 0; k < e.nsplit; ++k) {
-                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + ((first + 2 * k) * 128 + rr) * 2));
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-                                a.part + (((first + 2 * k) * (D / 4) + c4) * 128 + rr) * 4));
-                            const float w = ml.y == 0.f ? 0.f : ex2_approx(ml.x - M);
-                            if (ml.y != 0.f) {  // a part that sees no key of the row weighs nothing
-                                L += ml.y * w;
-                                A.x += v.x * w;
-                                A.y += v.y * w;
-                                A.z += v.z * w;
-                                A.w += v.w * w;
-                            }
-                        }
-                        const float li = L == 0.f ? 0.f : 1.f / L;
-                        const int rt = (128 * q + rr) / G, rh = g * G + (128 * q + rr) % G;
-                        uint2 w;
-                        w.x = pack_bf16(A.x * li, A.y * li);
-                        w.y = pack_bf16(A.z * li, A.w * li);
-                        *reinterpret_cast<uint2 *>(a.out + lr * a.o_l + (e.tok0 + rt) * a.o_t + rh * a.o_h + 4 * c4) = w;
-                        if (c4 == 0 && a.lse)
-                            a.lse[((long long)lr * a.n_tokens + e.tok0 + rt) * (a.n_kv * G) + rh] =
-                                L == 0.f ? NEG_INF : (M + log2f(L)) * 0.6931471805599453f;
-                    }
+                    const long long first = ((long long)ec.z * LH + (long long)lh * nsplit) * 2 + tile;
+                    chunk_merge<D>(a, first, nsplit, min(128, rows), wg_tid, G, r0, lr, g, ea.y);
                 }
             }
         }

@@ -408,3 +408,22 @@ def test_arguments_are_refused():
     assert (out == 7.0).all() and all(torch.equal(a, b) for a, b in zip(before, (pool.K, pool.V, pool.P, lens)))
     assert ctx.get_error()[0] == tri.TRI_OK
     ctx.close()
+
+
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+def test_a_key_that_is_not_finite_shows_in_every_row_that_sees_it(what):
+    """Whatever its place among the keys: NaN results, not a weight lost on the way."""
+    g = _gen(64)
+    ctx = pu.context(1, 1, 4, 64)
+    n, m = 3, 400
+    q = torch.full((1, n, 4, 64), 1.0, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, n], dtype=torch.int32).cuda()
+    lens = torch.tensor([m], dtype=torch.int32).cuda()
+    for at in list(range(0, 16)) + [63, 64, 127, 128, 200, 301, 396]:
+        pool = pu.Paged(g, 1, 1, 64, 16, [m])
+        u, o = pool.places(0, m)
+        pool.K[:, u[at], :, o[at]] = what
+        lse = torch.empty((1, n, 4), device="cuda")
+        out = ctx.chunk_attention(pool.K, pool.V, lens, q, cu, lse=lse, block_table=pool.table)
+        assert torch.isnan(out).all() and torch.isnan(lse).all(), at
+    ctx.close()
