@@ -72,6 +72,7 @@ struct tri_ctx {
     } ws_new_len, ws_plan, ws_part;
     std::vector<void *> ws_old;
     unsigned *d_ticket = nullptr;
+    bool chunk_ready[2] = {false, false};  // the attention kernels' shared memory has been opted in to
     // device bookkeeping
     unsigned long long *d_status = nullptr;
     // [0] CTAs of the fused kernel done, [1] its next free unit
@@ -1487,8 +1488,11 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
     }
     const unsigned smem = tri::chunk_smem(D).total;
     const void *fn = D == 128 ? (const void *)&tri::tri_chunk_kernel<128> : (const void *)&tri::tri_chunk_kernel<64>;
-    ce = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (ce != cudaSuccess) return cuda_fail(c, ce, "cudaFuncSetAttribute(chunk)");
+    if (!c->chunk_ready[D == 128]) {
+        ce = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (ce != cudaSuccess) return cuda_fail(c, ce, "cudaFuncSetAttribute(chunk)");
+        c->chunk_ready[D == 128] = true;
+    }
 
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -107,20 +107,6 @@ struct ChunkArgs {
 
 __host__ __device__ inline int chunk_blocks(int n, int G) { return (n + kChunkRows / G - 1) / (kChunkRows / G); }
 
-// The steps of warpgroup q in an item: `total` half tiles of 64 keys from the item's first on, cut off where
-// the last row of its query tile sees no further; of a paired item those of the tiles i with i % 2 == q.
-struct ChunkSteps {
-    int total;
-    __device__ __forceinline__ ChunkSteps(const ChunkEntry &e, int q, int G, int causal) {
-        const int r1 = e.pair ? e.ntok * G : min(128 * q + 128, e.ntok * G);
-        const int see = min(e.len, causal ? e.first + (r1 - 1) / G : e.len);
-        const bool rows = e.pair || r1 > 128 * q;
-        total = rows ? max(0, min(see, e.kt1 * 128) - e.kt0 * 128 + 63) / 64 : 0;
-    }
-    // half tiles of tile i
-    __device__ __forceinline__ int of(int i) const { return max(0, min(2, total - 2 * i)); }
-};
-
 // ---------------------------------------------------------------------------------
 // The plan.
 // ---------------------------------------------------------------------------------
@@ -367,13 +353,6 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
 // ---------------------------------------------------------------------------------
 // PTX of the attention kernel.
 // ---------------------------------------------------------------------------------
-__device__ __forceinline__ void tma_tile_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
-}
 __device__ __forceinline__ void tma_tile_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w,
                                             uint64_t *bar) {
     asm volatile(
@@ -389,22 +368,63 @@ constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_low(uint32_t smem_addr, unsigned lead_bytes) {
     return (smem_addr >> 4) | ((lead_bytes >> 4) << 16);
 }
-__device__ __forceinline__ void chunk_mma_ss(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, int acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_low), "r"(b_low), "r"(idesc), "r"(acc), "r"(kDescHigh)
-        : "memory");
-}
-// One thread of a converged warp, in the form from which the compiler knows that the code under it runs
-// once and keeps the operands of the MMAs in uniform registers (under a plain lane test it moved each
-// operand of each MMA over by itself: 94 clocks an MMA against 64 of the tensor core).
-__device__ __forceinline__ bool elect_one() {
+// In the roles below an instruction that one lane issues carries its predicate (`on`) with it instead of
+// standing in a branch: a warp that diverges and joins again around each of them lost more time in a
+// step than its MMAs take.
+__device__ __forceinline__ uint32_t elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
+    return p;
+}
+__device__ __forceinline__ void chunk_mma_ss(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, int acc,
+                                             uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_low), "r"(b_low), "r"(idesc), "r"(acc), "r"(kDescHigh), "r"(on)
+        : "memory");
+}
+// A (bf16 pairs, one row per lane) in tensor memory.
+__device__ __forceinline__ void chunk_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, int acc,
+                                             uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(acc), "r"(kDescHigh), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(uint64_t *bar, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void arrive_if(uint64_t *bar, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void expect_tx_if(uint64_t *bar, unsigned bytes, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "r"(bytes), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void tma_tile_2d_if(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];\n\t}" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "r"(on)
+        : "memory");
 }
 // Three-input maximum that keeps a NaN.
 __device__ __forceinline__ float max3nan(float a, float b, float c) {
@@ -492,7 +512,7 @@ __device__ __forceinline__ float2 exp2_pair(float2 x) {
                        __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
 }
 
-constexpr int kChunkEmu128 = 1, kChunkEmu64 = 2;
+constexpr int kChunkEmu128 = 1, kChunkEmu64 = 0;
 
 struct ChunkSmem {
     unsigned q, ring, ml, bars, total;
@@ -504,9 +524,9 @@ __host__ __device__ inline ChunkSmem chunk_smem(int D) {
     L.ring = 2u * (unsigned)D * 256u;               // two query tiles of 128 rows
     L.ml = L.ring + NST * (unsigned)D * 256u;  // a paired item's second (m, l) of each row
     L.bars = L.ml + 128u * 8u;
-    // full, empty [stages each], q full and empty, S and P full [4 each: warpgroup, half], P V and O done [2 each], done, parts written and merge
-    // decided [2 each], exchange full and free, TMEM address, abort, merge[2]
-    L.total = L.bars + (2u * NST + 21u) * 8u + 32u + 1024u;  // + alignment slack
+    // full, empty [stages each], q full and empty, S, P, most of P and O full [2 each], done, parts written and merge
+    // decided [2 each], exchange full and free, turns [2], TMEM address, abort, merge[2]
+    L.total = L.bars + (2u * NST + 19u) * 8u + 32u + 1024u;  // + alignment slack
     return L;
 }
 
@@ -552,20 +572,18 @@ __device__ __forceinline__ void chunk_row_again(const ChunkArgs &a, int s, int l
     }
 }
 
-// A step of one row, 64 keys: S from tensor memory, masked, into the running (m, l); P over S. `left`: the
-// step's keys that the row sees (cut: some row of the tile sees fewer than 64). `fresh`: the row's first step.
-// pv: completes a phase with every P V of the warpgroup, pv_parity that of the last step's (of which at most
-// that one is outstanding: this step's S followed the one before it).
+// A 128-key tile of one row: S from tensor memory, masked, into the running (m, l); P over S. `left`: the
+// tile's keys that the row sees (cut: some row of the tile sees fewer than 128). `fresh`: the first tile.
 //
-// The hardware exponential takes 8 clocks a warp, 512 for the step; `kEmu` of every 8 pairs are evaluated on the
-// FMA pipe instead.
+// The hardware exponential takes 8 clocks a warp, 1024 for the tile; `kEmu` of every 8 pairs are
+// evaluated on the FMA pipe instead, about where the two pipes finish together.
 template <int D>
-__device__ __forceinline__ bool chunk_softmax_step(uint32_t ts, uint32_t to, float c, bool cut, int left, bool fresh,
-                                                   float &m, float &l, uint64_t *pv, unsigned pv_parity, int tries) {
+__device__ __forceinline__ void chunk_softmax_tile(uint32_t ts, uint32_t to, float c, bool cut, int left, bool fresh,
+                                                   float &m, float &l, int lane, uint64_t *most) {
     constexpr unsigned FULL = 0xffffffffu;
     constexpr int kEmu = D == 128 ? kChunkEmu128 : kChunkEmu64;
     const float NEG_INF = __int_as_float(0xff800000);
-    uint32_t s0[32], s1[32];
+    uint32_t s0[32], s1[32], s2[32], s3[32];
     float x0 = NEG_INF, x1 = NEG_INF, x2 = NEG_INF, x3 = NEG_INF;
     auto top = [&](uint32_t(&s)[32], int at) {
         if (cut) {
@@ -582,18 +600,22 @@ __device__ __forceinline__ bool chunk_softmax_step(uint32_t ts, uint32_t to, flo
         }
     };
     tmem_ld32(ts, s0);
-    tmem_ld32(ts + 32u, s1);
     tmem_wait32(s0);
-    tmem_after32(s1);
+    tmem_ld32(ts + 32u, s1);
+    tmem_ld32(ts + 64u, s2);
+    tmem_ld32(ts + 96u, s3);
     top(s0, 0);
+    tmem_wait32(s1);
+    tmem_after32(s2);
+    tmem_after32(s3);
     top(s1, 32);
+    top(s2, 64);
+    top(s3, 96);
     const float mx = max3nan(max3nan(x0, x1, x2), x3, x3);
     if (fresh) {
         m = mx;
     } else if (__any_sync(FULL, mx != NEG_INF && !((mx - m) * c <= 8.f))) {
-        // once P V of the step before is complete, O is this warpgroup's to rescale
-        if (!__all_sync(FULL, mbar_wait_bounded(pv, pv_parity, tries))) return false;
-        tc_fence_after();
+        // P V of the tiles before is complete: O is this warpgroup's to rescale
         const float mn = max3nan(m, mx, mx);
         const float f = m == mn ? 1.f : ex2_approx((m - mn) * c);
         m = mn;
@@ -612,25 +634,36 @@ __device__ __forceinline__ bool chunk_softmax_step(uint32_t ts, uint32_t to, flo
     const float mc = m == NEG_INF ? 0.f : (m + (m - m)) * c;
     float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
     const float2 c2 = make_float2(c, c), m2 = make_float2(-mc, -mc);
-    uint32_t p[32];
-    auto weights = [&](const uint32_t(&s)[32], int at) {
+    uint32_t p[16];
+    auto weights = [&](const uint32_t(&s)[32], int from, int upto) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
+        for (int j = from; j < upto; j += 2) {
             float2 y = __ffma2_rn(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), c2, m2);
             if (j / 2 * kEmu % 8 + kEmu > 7 && kEmu > 0)
                 y = exp2_pair(y);
             else
                 y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
             if (j % 4 == 0) sum0 = __fadd2_rn(sum0, y); else sum1 = __fadd2_rn(sum1, y);
-            p[at + j / 2] = pack_bf16(y.x, y.y);
+            p[j / 2] = pack_bf16(y.x, y.y);
         }
     };
-    weights(s0, 0);
-    weights(s1, 16);
-    tmem_st32(ts, p);
+    weights(s0, 0, 32);
+    tmem_st16(ts, p);
+    weights(s1, 0, 32);
+    tmem_st16(ts + 16u, p);
+    weights(s2, 0, 32);
+    tmem_st16(ts + 32u, p);
+    // the first 96 keys' weights are handed over once their stores, by now under way for a while, are done,
+    // so that most of P V runs during the rest
+    weights(s3, 0, 16);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    arrive_if(most, lane == 0);
+    weights(s3, 16, 32);
+    tmem_st16(ts + 48u, p);
     l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
     tmem_wait_st();
-    return true;
 }
 
 // Join the parts of a block's row tile in the order of the keys: `first` + 2 k for k < nsplit. Each thread
@@ -713,16 +746,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint64_t *empty = full + NST;
     uint64_t *qfull = empty + NST;
     uint64_t *qempty = qfull + 1;
-    uint64_t *sfull = qempty + 1;   // [warpgroup][half]
-    uint64_t *pfull = sfull + 4;    // [warpgroup][half]
-    uint64_t *pv = pfull + 4;       // [warpgroup]
-    uint64_t *ofull = pv + 2;       // [warpgroup]
+    uint64_t *sfull = qempty + 1;   // [2]
+    uint64_t *pfull = sfull + 2;    // [2]
+    uint64_t *pmost = pfull + 2;    // [2]
+    uint64_t *ofull = pmost + 2;    // [2]
     uint64_t *done = ofull + 2;
     uint64_t *parts = done + 1;     // [2]
     uint64_t *decided = parts + 2;  // [2]
     uint64_t *xfull = decided + 2;
     uint64_t *xfree = xfull + 1;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(xfree + 1);
+    uint64_t *turn = xfree + 1;     // [2]
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(turn + 2);
     float2 *ml_x = reinterpret_cast<float2 *>(smem + Ly.ml);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     volatile int *merge_flag = abort_flag + 1;        // [2]
@@ -735,15 +769,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         mbar_init(qfull, 1);
         mbar_init(qempty, 2);        // an arrival of each MMA warp
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(sfull + i, 1);
             mbar_init(pfull + i, 4);  // the warpgroup's warps
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(pv + i, 1);
+            mbar_init(pmost + i, 4);
             mbar_init(ofull + i, 1);
             mbar_init(parts + i, 4);
             mbar_init(decided + i, 1);
+            mbar_init(turn + i, 1);
         }
         mbar_init(done, 2);
         mbar_init(xfull, 4);
@@ -827,15 +860,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     if (lane == 0) fail(e, lh);
                     return false;
                 }
-                if (lane == 0) {
-                    // the MMA warp may have written zeros to this stage (generic proxy)
-                    fence_proxy_async_smem();
-                    mbar_expect_tx(full + st, (unsigned)(pieces * pr) * 128u * KCH);
-                }
+                // (an MMA warp may have written zeros to this stage with the generic proxy)
+                fence_proxy_async_smem();
+                expect_tx_if(full + st, (unsigned)(pieces * pr) * 128u * KCH, lane == 0);
                 __syncwarp();
-                if (p < np && r0 < e.len && !skip)
-                    tma_tile_2d(smem + Ly.ring + (unsigned)st * kTileBytes + c * kChunkBytes + (unsigned)(p * pr) * 128u, map,
-                                c * 64, (int)row, full + st);
+                tma_tile_2d_if(smem + Ly.ring + (unsigned)st * kTileBytes + c * kChunkBytes + (unsigned)(p * pr) * 128u, map,
+                                c * 64, (int)row, full + st, p < np && r0 < e.len && !skip);
                 ++k;
                 fill.step();
                 return true;
@@ -858,23 +888,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (nq > 0) (void)mbar_wait_bounded(qfull, (unsigned)((nq - 1) & 1), a.wait_tries);
         __syncwarp();
     } else if (warp <= 2) {
-        // ---------------- MMAs: one warp for each warpgroup's, so that one's waits and bookkeeping run beside
-        // the other's MMAs
+        // ---------------- MMAs: one warp for each warpgroup's, so that one's bookkeeping and waits run beside
+        // the other's MMAs (a single warp left the tensor core idle for about 900 of 4100 clocks a round)
         const int q = warp - 1;
-        const uint32_t id_s = mx_idesc(64), id_o = mx_idesc(D) | (1u << 16);  // V is N-major
+        const uint32_t id_s = mx_idesc(128), id_o = mx_idesc(D) | (1u << 16);  // V is N-major
         const uint32_t q_low = desc_low(smem_u32(smem + Ly.q), 16u), k_low = desc_low(smem_u32(smem + Ly.ring), 16u);
         const uint32_t v_low = desc_low(smem_u32(smem + Ly.ring), kChunkBytes);
         const uint32_t sd = tmem + 128u * q, od = tmem + 256u + (uint32_t)(D * q);
+        const uint32_t lead_lane = elect_one();
         ChunkRing<NST> at;            // the next tile
-        unsigned nq = 0, np0 = 0, np1 = 0;  // items, P of each half so far
+        unsigned nq = 0, np = 0;      // items, P tiles so far
+        unsigned nt = 0;              // turns waited for
+        bool owed = false;            // the other warp's turn comes before this one's next
         bool ok = true;
         auto wait = [&](uint64_t *bar, unsigned phase) {
             return __all_sync(FULL, mbar_wait_bounded(bar, phase & 1u, a.wait_tries));
         };
-        // a tile that this warp does not use: its release takes an arrival of each
+        // a tile that is the other warp's: its release takes an arrival of each
         auto skip = [&] {
             ok = ok && wait(full + at.stage, at.phase);
-            if (ok && lane == 0) mbar_arrive(empty + at.stage);
+            arrive_if(empty + at.stage, ok && lane == 0);
             at.step();
         };
         for (int r = 0; ok && !*abort_flag; ++r) {
@@ -885,103 +918,94 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const int n = __shfl_sync(FULL, e.kt1 - e.kt0, 0);
             if (n <= 0) continue;
             const bool pair = __shfl_sync(FULL, e.pair, 0) != 0;
+            const bool both = pair || __shfl_sync(FULL, e.ntok * G, 0) > 128, idle = q == 1 && !both;
             const int lead = pair ? 2 : 1, left = __shfl_sync(FULL, e.len - e.kt0 * 128, 0);
-            ChunkSteps steps(e, q, G, a.causal);
-            steps.total = __shfl_sync(FULL, steps.total, 0);
             const uint32_t ql = q_low + (pair ? 0u : (uint32_t)q * (kTileBytes >> 4));
-            // S of 64 keys into its half of the warpgroup's columns
-            auto mma_s = [&](uint32_t bl, int h) {
+            auto mma_s = [&](uint32_t bl, uint32_t on) {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const unsigned off = ((unsigned)(ks >> 2) * kChunkBytes + (unsigned)(ks & 3) * 32u) >> 4;
-                    chunk_mma_ss(sd + 64u * h, ql + off, bl + h * 512u + off, id_s, ks > 0);
+                    chunk_mma_ss(sd, ql + off, bl + off, id_s, ks > 0, on);
                 }
-                mx_commit(sfull + 2 * q + h);
+                commit_if(sfull + q, on);
             };
-            auto mine = [&](int i) { return pair && (i & 1) != q ? 0 : steps.of(i); };
             ok = wait(qfull, nq);
             ++nq;
-            bool used = false;        // the query tile
-            for (int t = 0; ok && t < lead; ++t) {
-                const int hs = mine(t);
-                if (hs == 0) {
-                    skip();
-                    continue;
-                }
-                used = true;
-                ok = wait(full + at.stage, at.phase);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t bl = __shfl_sync(FULL, k_low + (unsigned)at.stage * (kTileBytes >> 4), 0);
-                if (elect_one()) {
-                    mma_s(bl, 0);
-                    if (hs > 1) mma_s(bl, 1);
-                    mx_commit(empty + at.stage);
-                    if (t + lead >= n || mine(t + lead) == 0) mx_commit(qempty);
-                }
-                __syncwarp();
-                at.step();
-            }
-            if (ok && !used && lane == 0) mbar_arrive(qempty);
-            for (int i = 0; ok && i < n; ++i) {
-                const bool more = i + lead < n;
-                const int hs = mine(i), hn = more ? mine(i + lead) : 0;
-                if (hs == 0) {
-                    skip();
-                    if (more) skip();
-                    continue;
-                }
-                const ChunkRing<NST> av = at;  // this tile's V; `at`: the K `lead` tiles on
-                at.step();
-                ok = wait(full + av.stage, av.phase);
-                if (!ok) break;
-                // value rows past the length hold whatever was there: zero them, for a zero weight does
-                // not clear a NaN (both warps of a tile that they share write the same zeros)
-                const int valid = left - i * 128;
-                if (valid < 128) {
-                    unsigned char *Vs = smem + Ly.ring + (unsigned)av.stage * kTileBytes;
-                    const int words = (128 - valid) * 8;  // 16-byte words of a chunk
-                    for (int w = lane; w < words * KCH; w += 32) {
-                        const int c = w / words, x = w % words;
-                        *reinterpret_cast<uint4 *>(Vs + c * kChunkBytes + (unsigned)valid * 128u + (unsigned)x * 16u) =
-                            make_uint4(0u, 0u, 0u, 0u);
+            if (!ok || idle) {
+                for (int i = 0; ok && i < 2 * n; ++i) skip();
+                arrive_if(qempty, ok && lane == 0);
+            } else {
+                // the last key tile of this warp: after it the query tile is free
+                const int end = pair ? n - 1 - ((n - 1 - q) & 1) : n - 1;
+                for (int t = 0; ok && t < lead; ++t) {
+                    if (pair && t != q) {
+                        skip();
+                        continue;
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                const uint32_t vl = __shfl_sync(FULL, v_low + (unsigned)av.stage * (kTileBytes >> 4), 0);
-                const uint32_t bl = __shfl_sync(FULL, k_low + (unsigned)at.stage * (kTileBytes >> 4), 0);
-                ok = !hn || wait(full + at.stage, at.phase);
-                if (!ok) break;
-                auto half = [&](int h, unsigned &np) {
-                    ok = wait(pfull + 2 * q + h, np);
-                    ++np;
-                    if (!ok) return;
+                    ok = wait(full + at.stage, at.phase);
+                    if (!ok) break;
                     tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)  // 16 keys: 16 rows of 128 bytes of each chunk
-                            chunk_mma_ts(od, sd + 64u * h + 8u * ks, vl + (4 * h + ks) * 128u, id_o,
-                                         (i >= lead || h > 0 || ks > 0));
-                        mx_commit(pv + q);
-                        if (hn > h) mma_s(bl, h);
-                        if (h + 1 == hs) {
-                            mx_commit(empty + av.stage);
-                            if (!hn) {
-                                mx_commit(ofull + q);
-                            } else {
-                                mx_commit(empty + at.stage);
-                                if (i + 2 * lead >= n || mine(i + 2 * lead) == 0) mx_commit(qempty);
-                            }
-                        }
+                    const uint32_t bl = __shfl_sync(FULL, k_low + (unsigned)at.stage * (kTileBytes >> 4), 0);
+                    mma_s(bl, lead_lane);
+                    commit_if(empty + at.stage, lead_lane);
+                    commit_if(qempty, lead_lane && t == end);
+                    at.step();
+                }
+                for (int i = 0; ok && i < n; ++i) {
+                    const bool more = i + lead < n;
+                    if (pair && (i & 1) != q) {
+                        skip();
+                        if (more) skip();
+                        continue;
                     }
-                    __syncwarp();
-                };
-                half(0, np0);
-                if (ok && hs > 1) half(1, np1);
-                if (!ok) break;
-                if (hn) at.step();
-                else if (more) skip();
+                    const ChunkRing<NST> av = at;  // this tile's V; `at`: the K `lead` tiles on
+                    at.step();
+                    ok = wait(full + av.stage, av.phase);
+                    if (!ok) break;
+                    // value rows past the length hold whatever was there: zero them, for a zero weight does
+                    // not clear a NaN (both warps of a tile that they share write the same zeros)
+                    const int valid = left - i * 128;
+                    if (valid < 128) {
+                        unsigned char *Vs = smem + Ly.ring + (unsigned)av.stage * kTileBytes;
+                        const int words = (128 - valid) * 8;  // 16-byte words of a chunk
+                        for (int w = lane; w < words * KCH; w += 32) {
+                            const int c = w / words, x = w % words;
+                            *reinterpret_cast<uint4 *>(Vs + c * kChunkBytes + (unsigned)valid * 128u + (unsigned)x * 16u) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    const uint32_t vl = __shfl_sync(FULL, v_low + (unsigned)av.stage * (kTileBytes >> 4), 0);
+                    const uint32_t bl = __shfl_sync(FULL, k_low + (unsigned)at.stage * (kTileBytes >> 4), 0);
+                    ok = (!more || wait(full + at.stage, at.phase)) && wait(pmost + q, np);
+                    // the two warps take turns: MMAs of both at once would share the tensor core, end together
+                    // and leave it idle while both warpgroups exponentiate
+                    if (ok && (q == 1 || owed)) ok = wait(turn + (q ^ 1), nt++);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < 6; ++ks)  // 16 keys: 16 rows of 128 bytes of each chunk
+                        chunk_mma_ts(od, sd + 8u * ks, vl + ks * 128u, id_o, (i >= lead || ks > 0), lead_lane);
+                    ok = wait(pfull + q, np);
+                    ++np;
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 6; ks < 8; ++ks) chunk_mma_ts(od, sd + 8u * ks, vl + ks * 128u, id_o, 1, lead_lane);
+                    if (more) {
+                        mma_s(bl, lead_lane);
+                        commit_if(empty + av.stage, lead_lane);
+                        commit_if(empty + at.stage, lead_lane);
+                        commit_if(qempty, lead_lane && i + lead == end);
+                    } else {
+                        commit_if(ofull + q, lead_lane);
+                        commit_if(empty + av.stage, lead_lane);
+                    }
+                    owed = q == 0 && (pair ? i + 1 < n : both);
+                    arrive_if(turn + q, lane == 0 && (q == 1 || owed));
+                    if (more) at.step();
+                }
             }
             if (!ok) {
                 if (lane == 0) fail(e, (int)(it % LH));
@@ -989,7 +1013,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
         }
         // MMAs may still run (after a wait that ran out): they must end before the TMEM is released
-        if (elect_one()) mx_commit(done);
+        commit_if(done, lead_lane);
         __syncwarp();
         (void)mbar_wait_bounded(done, 0u, a.wait_tries);
         __syncwarp();
@@ -1002,7 +1026,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + 128u * q, to = tmem + lanes + 256u + (uint32_t)(D * q);
         const int wg_tid = tid & 127;
-        unsigned ns0 = 0, ns1 = 0, no = 0, nm = 0, nx = 0;  // S of each half, items, items in parts, paired items so far
+        unsigned ns = 0, no = 0, nm = 0, nx = 0;  // S tiles, items, items in parts, paired items so far
         bool ok = true;
         for (int r = 0; ok && !*abort_flag; ++r) {
             const long long it = item_of(r);
@@ -1011,7 +1035,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const int lh = (int)(it % LH);
             float m = NEG_INF, l = 0.f;
             int n, rows, limit;
-            bool pair, any;                                   // any: the warpgroup had steps (O holds something)
+            bool pair;
             {
                 const ChunkEntry e = *ep;
                 pair = e.pair;
@@ -1022,30 +1046,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 limit = min(e.len, a.causal ? e.first + (r0 + row) / G : e.len);
                 const int sure = min(e.len, a.causal ? e.first + r0 / G : e.len);  // seen by every row
                 const bool work = (warp & 3) * 32 < rows;     // a warp without rows only keeps the step
-                const ChunkSteps steps(e, q, G, a.causal);
                 const int step = pair ? 2 : 1;
-                bool fresh = true;
-                for (int i = pair ? q : 0; ok && i < n; i += step) {
-                    const int hs = steps.of(i);
-                    for (int h = 0; ok && h < hs; ++h) {
-                        ok = __all_sync(FULL, mbar_wait_bounded(sfull + 2 * q + h, (h ? ns1 : ns0) & 1u, a.wait_tries));
-                        if (!ok) break;
-                        if (work) {
-                            tc_fence_after();
-                            const int key0 = (e.kt0 + i) * 128 + 64 * h;
-                            ok = chunk_softmax_step<D>(ts + 64u * h, to, a.c, key0 + 64 > sure, limit - key0, fresh, m, l,
-                                                       pv + q, (ns0 + ns1 - 1u) & 1u, a.wait_tries);
-                            if (!ok) break;
-                            tc_fence_before();
-                        }
-                        if (h) ++ns1; else ++ns0;
-                        fresh = false;
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(pfull + 2 * q + h);
+                for (int i = pair ? q : 0; i < n; i += step) {
+                    ok = __all_sync(FULL, mbar_wait_bounded(sfull + q, ns & 1u, a.wait_tries));
+                    if (!ok) break;
+                    ++ns;
+                    if (work) {
+                        tc_fence_after();
+                        const int key0 = (e.kt0 + i) * 128;
+                        chunk_softmax_tile<D>(ts, to, a.c, key0 + 128 > sure, limit - key0, i < step, m, l, lane, pmost + q);
+                        tc_fence_before();
+                    } else {
+                        arrive_if(pmost + q, lane == 0);
                     }
+                    __syncwarp();
+                    arrive_if(pfull + q, lane == 0);
                 }
-                any = !fresh;
-                if (ok && any) {
+                if (ok && n > (pair ? q : 0)) {
                     ok = __all_sync(FULL, mbar_wait_bounded(ofull + q, no & 1u, a.wait_tries));
                     ++no;
                     tc_fence_after();
@@ -1104,7 +1121,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t o[32];
-                    if (any) {
+                    if (n > 0) {
                         tmem_ld32(to + c0, o);
                         tmem_wait32(o);
                         if (pair) {

@@ -312,21 +312,20 @@ def make_kv(K, V, pos, lens, lens_out=None, block_table=None, n_pages=None, laye
     return kv
 
 
-def make_rows(x: torch.Tensor, name: str = "x") -> tri_rows:
+def make_rows(x: torch.Tensor, name: str = "x", device: Optional[int] = None) -> tri_rows:
     """Describe bf16 rows held in a torch tensor [tokens][heads][d] or [layers][tokens][heads][d]: any strides that are
     multiples of 8 elements, each row contiguous."""
-    if x.dtype != torch.bfloat16 or not x.is_cuda or x.dim() not in (3, 4):
-        raise ValueError(f"{name} must be a CUDA tensor of torch.bfloat16 [tokens][heads][d] or [layers][tokens][heads][d]")
     shape, stride = x.shape, x.stride()
+    n = len(shape)
+    if x.dtype is not torch.bfloat16 or not x.is_cuda or n not in (3, 4):
+        raise ValueError(f"{name} must be a CUDA tensor of torch.bfloat16 [tokens][heads][d] or [layers][tokens][heads][d]")
+    if device is not None and x.get_device() != device:
+        raise ValueError(f"{name} is on {x.device}, the context on cuda:{device}")
     if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    r = tri_rows()
-    r.data = x.data_ptr()
-    # a dimension of one element has no stride of its own
-    r.head_stride = stride[-2] if shape[-2] > 1 else 0
-    r.token_stride = stride[-3] if shape[-3] > 1 else 0
-    r.layer_stride = stride[0] if len(shape) == 4 and shape[0] > 1 else 0
-    return r
+    # (data, layer, token and head stride: a dimension of one element has no stride of its own)
+    return tri_rows(x.data_ptr(), stride[0] if n == 4 and shape[0] > 1 else 0, stride[-3] if shape[-3] > 1 else 0,
+                    stride[-2] if shape[-2] > 1 else 0)
 
 
 class TriContext:
@@ -339,10 +338,11 @@ class TriContext:
 
     def _heads(self, name, q, n_kv):
         # the C ABI takes the head counts from the statistics: what the tensors hold must agree
-        if self.shape is not None and (int(q.shape[-2]), n_kv, int(q.shape[-1])) != (
-                self.shape[1] * self.shape[2], self.shape[1], self.shape[3]):
-            raise ValueError(f"{name} and the cache have {q.shape[-2]} and {n_kv} heads of {q.shape[-1]}, the loaded "
-                             f"statistics {self.shape[1] * self.shape[2]} and {self.shape[1]} of {self.shape[3]}")
+        Hq, d = q.shape[-2], q.shape[-1]
+        if self.shape is not None and (Hq, n_kv, d) != (self.shape[1] * self.shape[2], self.shape[1], self.shape[3]):
+            raise ValueError(f"{name} and the cache have {Hq} and {n_kv} heads of {d}, the loaded statistics "
+                             f"{self.shape[1] * self.shape[2]} and {self.shape[1]} of {self.shape[3]}")
+        return Hq
 
     def close(self):
         if self.handle is not None:
@@ -455,18 +455,41 @@ class TriContext:
             raise TriError(st, "tri_decode_attention", tri_last_error(self.handle))
         return out
 
-    def _vector(self, name, x, n):
-        if x.dtype != torch.int32 or not x.is_cuda or not x.is_contiguous() or x.dim() != 1 or x.shape[0] != n:
-            raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of {n} elements, got {tuple(x.shape)} {x.dtype}")
+    def _flat(self, name, x, dtype, shape=None):
+        if x.dtype is not dtype or x.get_device() != self.device or not x.is_contiguous() or (
+                shape is not None and x.shape != shape):
+            raise ValueError(f"{name} must be a contiguous tensor of {dtype} on cuda:{self.device}"
+                             + (f" shaped {tuple(shape)}" if shape is not None else "")
+                             + f", got {tuple(x.shape)} of {x.dtype} on {x.device}")
         return x.data_ptr()
 
-    def _here(self, **tensors):
-        for name, x in tensors.items():
-            if x is not None and x.device.index != self.device:
-                raise ValueError(f"{name} is on {x.device}, the context on cuda:{self.device}")
-
     def _stream(self, stream):
-        return (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.device) if stream is None else stream.cuda_stream
+
+    def _cache(self, K, V, pos, lens, lens_out, block_table, n_pages, layer_begin):
+        """The cache of a call (as make_kv, on this context's device), its layers, KV heads, head_dim and sequences."""
+        shape, batch = K.shape, lens.shape
+        if len(shape) != 5 or len(batch) != 1:
+            raise ValueError("K and V must be 5-D: [L][batch][Hkv][cap][d] dense or [L][pages][Hkv][page][d] paged, lens 1-D")
+        L, units, H, rows, d = shape
+        B = batch[0]
+        if block_table is None:
+            if units != B:
+                raise ValueError(f"dense cache holds {units} sequences, lens describes {B}")
+            table, cap, page, max_pages, n_pages = None, rows, 0, 0, 0
+        else:
+            if block_table.dim() != 2 or block_table.shape[0] != B:
+                raise ValueError(f"block_table must be [batch={B}][max_pages]")
+            if n_pages is not None and n_pages > units:
+                raise ValueError(f"n_pages is {n_pages}, the pools hold {units}")
+            table, cap, page, max_pages = self._flat("block_table", block_table, torch.int32), 0, rows, block_table.shape[1]
+            n_pages = units if n_pages is None else n_pages
+        kv = tri_kv(self._flat("K", K, torch.bfloat16), self._flat("V", V, torch.bfloat16, shape),
+                    None if pos is None else self._flat("pos", pos, torch.int32, shape[:4]),
+                    self._flat("lens", lens, torch.int32),
+                    None if lens_out is None else self._flat("lens_out", lens_out, torch.int32, batch), table, B, cap, page,
+                    max_pages, n_pages, layer_begin, L)
+        return kv, L, H, d, B
 
     def rope_load(self, omega, layout, magnitude=1.0):
         """The rotation of :meth:`rope` and :meth:`append_chunk`: omega fp64 [rotary_dim/2] radians per position (e.g. of
@@ -482,11 +505,10 @@ class TriContext:
             out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         if out.shape != x.shape:
             raise ValueError(f"out must be shaped like x {tuple(x.shape)}, got {tuple(out.shape)}")
-        self._here(x=x, pos=pos, out=out)
-        rows, rout = make_rows(x, "x"), make_rows(out, "out")
+        rows, rout = make_rows(x, "x", self.device), make_rows(out, "out", self.device)
         T, H, d = x.shape[-3:]
-        st = tri_rope(self.handle, rows, rout, x.shape[0] if x.dim() == 4 else 1, T, H, d, self._vector("pos", pos, T),
-                      inverse, self._stream(stream))
+        st = _lib.tri_rope(self.handle, rows, rout, x.shape[0] if x.dim() == 4 else 1, T, H, d,
+                           self._flat("pos", pos, torch.int32, (T,)), bool(inverse), self._stream(stream))
         if not check:
             return st
         if st != TRI_OK:
@@ -494,9 +516,10 @@ class TriContext:
         return out
 
     def _tokens(self, name, x, L, T, heads, d):
-        if (tuple(x.shape[-3:]) != (T, heads, d) if heads else x.shape[-1] != d) or (x.shape[0] if x.dim() == 4 else 1) != L:
-            raise ValueError(f"{name} must be [{L} layers][{T} tokens][{heads or 'heads'}][{d}], got {tuple(x.shape)}")
-        return make_rows(x, name)
+        shape = x.shape
+        if len(shape) not in (3, 4) or shape[-3:] != (T, heads, d) or (shape[0] if len(shape) == 4 else 1) != L:
+            raise ValueError(f"{name} must be [{L} layers][{T} tokens][{heads}][{d}], got {tuple(shape)}")
+        return make_rows(x, name, self.device)
 
     def append_chunk(self, K, V, pos, lens, K_new, V_new, cu_new, pos_new, block_table=None, lens_out="inplace",
                      rotate=True, q=None, q_out=None, n_pages=None, layer_begin=0, stream=None, check=True):
@@ -506,22 +529,17 @@ class TriContext:
         (rows of the query heads) is then rotated into q_out in the same launch (q_out=None: in place)."""
         if isinstance(lens_out, str):
             lens_out = lens
-        kv = make_kv(K, V, pos, lens, lens_out, block_table, n_pages=n_pages, layer_begin=layer_begin)
-        L, H, d, T, B = int(K.shape[0]), int(K.shape[2]), int(K.shape[4]), int(K_new.shape[-3]), int(lens.shape[0])
-        self._here(K=K, V=V, pos=pos, lens=lens, lens_out=lens_out, block_table=block_table, K_new=K_new, V_new=V_new,
-                   cu_new=cu_new, pos_new=pos_new, q=q, q_out=q_out)
+        kv, L, H, d, B = self._cache(K, V, pos, lens, lens_out, block_table, n_pages, layer_begin)
+        T = K_new.shape[-3]
         kn, vn = self._tokens("K_new", K_new, L, T, H, d), self._tokens("V_new", V_new, L, T, H, d)
-        if lens_out is not None and lens_out.shape != lens.shape:
-            raise ValueError("lens_out must be shaped like lens")
         qr = qo = None
         if q is not None:
             q_out = q if q_out is None else q_out
-            if q_out.shape != q.shape or q.shape[-2] % H:
-                raise ValueError(f"q_out must be shaped like q {tuple(q.shape)}, its heads a multiple of {H}")
-            qr, qo = self._tokens("q", q, L, T, int(q.shape[-2]), d), self._tokens("q_out", q_out, L, T, int(q.shape[-2]), d)
-            self._heads("q", q, H)
-        st = tri_append_chunk(self.handle, kv, kn, vn, self._vector("cu_new", cu_new, B + 1),
-                              self._vector("pos_new", pos_new, T), T, bool(rotate), qr, qo, self._stream(stream))
+            Hq = self._heads("q", q, H)
+            qr, qo = self._tokens("q", q, L, T, Hq, d), self._tokens("q_out", q_out, L, T, Hq, d)
+        st = _lib.tri_append_chunk(self.handle, kv, kn, vn, self._flat("cu_new", cu_new, torch.int32, (B + 1,)),
+                                   self._flat("pos_new", pos_new, torch.int32, (T,)), T, bool(rotate), qr, qo,
+                                   self._stream(stream))
         if check and st != TRI_OK:
             raise TriError(st, "tri_append_chunk", tri_last_error(self.handle))
         return st
@@ -532,18 +550,18 @@ class TriContext:
         sequence s holding the tokens [cu_q[s], cu_q[s + 1])) over the cache that already holds those tokens as the
         last of its lens[s] rows. scale: of the logits (None: 1/sqrt(d)); lse: fp32 [n_layers][tokens][Hq] to receive
         the logarithm of the softmax sums. Returns out (bf16, like q), or the status when check is False."""
-        kv = make_kv(K, V, None, lens, None, block_table, n_pages=n_pages, layer_begin=layer_begin)
-        L, H, d, B = int(K.shape[0]), int(K.shape[2]), int(K.shape[4]), int(lens.shape[0])
-        T, Hq = int(q.shape[-3]), int(q.shape[-2])
+        kv, L, H, d, B = self._cache(K, V, None, lens, None, block_table, n_pages, layer_begin)
+        T = q.shape[-3]
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        self._here(K=K, V=V, lens=lens, block_table=block_table, q=q, cu_q=cu_q, out=out, lse=lse)
+        Hq = self._heads("q", q, H)
         qr, ro = self._tokens("q", q, L, T, Hq, d), self._tokens("out", out, L, T, Hq, d)
-        self._heads("q", q, H)
-        if lse is not None and (lse.dtype != torch.float32 or lse.numel() != L * T * Hq or not lse.is_contiguous()):
-            raise ValueError(f"lse must be a contiguous float32 tensor [{L}][{T}][{Hq}]")
-        st = tri_chunk_attention(self.handle, kv, qr, self._vector("cu_q", cu_q, B + 1), T,
-                                 d ** -0.5 if scale is None else scale, bool(causal), ro, _ptr(lse), self._stream(stream))
+        if lse is not None and (lse.dtype is not torch.float32 or lse.numel() != L * T * Hq or not lse.is_contiguous()
+                                or lse.get_device() != self.device):
+            raise ValueError(f"lse must be a contiguous float32 tensor [{L}][{T}][{Hq}] on cuda:{self.device}")
+        st = _lib.tri_chunk_attention(self.handle, kv, qr, self._flat("cu_q", cu_q, torch.int32, (B + 1,)), T,
+                                      d ** -0.5 if scale is None else scale, bool(causal), ro,
+                                      None if lse is None else lse.data_ptr(), self._stream(stream))
         if not check:
             return st
         if st != TRI_OK:
