@@ -1443,7 +1443,8 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
     a.max_slots = 4 * c->sm_count;
     const long long blocks = (long long)n_tokens * G / tri::kChunkRows + kv->batch;
     const long long entries = blocks + a.max_slots;
-    if (entries * L * Hkv > (1LL << 40) || entries > (1LL << 30)) return TRI_EUNSUPPORTED;
+    // items and key tiles are counted in 32 bits
+    if (entries * L * Hkv >= (1LL << 30) || blocks * ((cap_u + 127) / 128 + 4) >= (1LL << 31)) return TRI_EUNSUPPORTED;
     a.max_entries = (int)entries;
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -1453,7 +1454,7 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
     };
     const size_t o_head = take(sizeof(tri::ChunkHead)), o_seqs = take(sizeof(tri::ChunkSeq) * (size_t)kv->batch),
                  o_base = take(sizeof(int) * ((size_t)kv->batch + 1)), o_tiles = take(sizeof(int) * (size_t)blocks),
-                 o_counters = take(sizeof(unsigned) * 2 * (size_t)a.max_slots),
+                 o_merges = take(sizeof(tri::ChunkEntry) * (size_t)a.max_slots),
                  o_entries = take(sizeof(tri::ChunkEntry) * (size_t)entries);
     const size_t part_floats = (size_t)a.max_slots * 2 * 128 * D, ml_floats = (size_t)a.max_slots * 2 * 128 * 2;
     const bool fresh = off > c->ws_plan.bytes;
@@ -1465,7 +1466,7 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
     a.seqs = reinterpret_cast<tri::ChunkSeq *>(ws + o_seqs);
     a.base = reinterpret_cast<int *>(ws + o_base);
     a.tiles = reinterpret_cast<int *>(ws + o_tiles);
-    a.counters = reinterpret_cast<unsigned *>(ws + o_counters);
+    a.merges = reinterpret_cast<tri::ChunkEntry *>(ws + o_merges);
     a.entries = reinterpret_cast<tri::ChunkEntry *>(ws + o_entries);
     a.part = static_cast<float *>(c->ws_part.p);
     a.part_ml = a.part + part_floats;
@@ -1499,7 +1500,10 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3((unsigned)kv->batch);
+    // one CTA for a small plan (no hand-over between CTAs: 3 us less), else one per sequence
+    const bool alone = kv->batch <= tri::kChunkPlanSeqs &&
+                       (!paged || (long long)kv->batch * kv->max_pages <= tri::kChunkPlanAlone);
+    cfg.gridDim = dim3(alone ? 1u : (unsigned)kv->batch);
     cfg.blockDim = dim3((unsigned)tri::kChunkPlanThreads);
     cfg.stream = cs;
     cfg.attrs = pdl;
@@ -1512,6 +1516,12 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
     void *params[] = {&qmap, &kmap, &vmap, &a};
     ce = cudaLaunchKernelExC(&cfg, fn, params);
     if (ce != cudaSuccess) return cuda_fail(c, ce, "launch(chunk attention)");
+    cfg.gridDim = dim3((unsigned)(4 * c->sm_count));
+    cfg.blockDim = dim3((unsigned)tri::kChunkMergeThreads);
+    cfg.dynamicSmemBytes = 0;
+    ce = D == 128 ? cudaLaunchKernelEx(&cfg, tri::tri_chunk_merge_kernel<128>, a)
+                  : cudaLaunchKernelEx(&cfg, tri::tri_chunk_merge_kernel<64>, a);
+    if (ce != cudaSuccess) return cuda_fail(c, ce, "launch(chunk merge)");
     return TRI_OK;
 }
 

@@ -62,7 +62,7 @@ struct __align__(16) ChunkEntry {
     int s, tok0, ntok, len;   // sequence, first token (global row), tokens of the block, cached rows
     int first, kt0, kt1;      // keys seen by the block's first row, key tiles
     int pair;                 // one row tile whose key tiles the two warpgroups take in turn
-    int nsplit, split, slot, group;  // splits of the block; this one; its first partial; its counter
+    int nsplit, split, slot, unused;  // splits of the block; this one; its first partial
 };
 
 struct __align__(16) ChunkSeq {
@@ -71,6 +71,7 @@ struct __align__(16) ChunkSeq {
 
 struct ChunkHead {
     int n_entries;            // lines of the plan
+    int n_groups;             // blocks that are split
     unsigned ticket;          // plan CTAs done (back to 0 at the end)
 };
 
@@ -99,7 +100,7 @@ struct ChunkArgs {
     ChunkEntry *entries;
     float *part;              // [slot][tile][D / 4][128][4], then [slot][tile][128][2] (m, l)
     float *part_ml;
-    unsigned *counters;       // [group][tile]
+    ChunkEntry *merges;       // the blocks that are split
     unsigned long long *status;
     int wait_tries;
     long long inject_unit;
@@ -112,10 +113,12 @@ __host__ __device__ inline int chunk_blocks(int n, int G) { return (n + kChunkRo
 // ---------------------------------------------------------------------------------
 // Costs in units of one key tile of an item: what a further item costs its CTA (filling and draining
 // the pipeline, the result), and what the merge of a split adds at the end.
-constexpr int kChunkItemCost = 2;
-constexpr int kChunkMergeCost = 2, kChunkMergeRows = 4;  // a merge: the first, and the second for a full block
+constexpr int kChunkItemCost = 3;
+constexpr int kChunkMergeCost = 3, kChunkMergeRows = 2;  // a merge: the first, and the second for a full block
 constexpr int kChunkPlanSeqs = 512, kChunkPlanBlocks = 2048;  // what the plan keeps in shared memory, at most
 constexpr int kChunkSortBins = 1024;
+constexpr int kChunkCandidates = 16;
+constexpr int kChunkPlanAlone = 8192;  // block table entries that one CTA checks by itself
 
 __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const ChunkArgs a) {
     constexpr unsigned FULL = 0xffffffffu;
@@ -123,15 +126,50 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
     __shared__ int hist[kChunkSortBins];
     __shared__ ChunkSeq sh_seqs[kChunkPlanSeqs];
     __shared__ int sh_base[kChunkPlanSeqs + 1], sh_tiles[kChunkPlanBlocks];
-    __shared__ long long est[8];
-    __shared__ int est_chunk[8];
+    __shared__ float est[kChunkCandidates];
+    __shared__ int est_chunk[kChunkCandidates];
     __shared__ long long sh_sum;
     __shared__ int sh_max, sh_entries, sh_slots, sh_groups, sh_chunk;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int s0 = blockIdx.x;
-    {
+    const bool alone = gridDim.x == 1;  // one CTA checks every sequence (it needs no hand-over between CTAs)
+    if (alone) {
+        // (one CTA only where its shared memory holds the sequences)
+        for (int s = tid; s < a.batch; s += kChunkPlanThreads) {
+            const int lo = __ldg(a.cu + s), hi = __ldg(a.cu + s + 1), len = __ldg(a.lens + s);
+            const int bad = lo < 0 || lo > hi || hi > a.n_tokens ? kDevBadRange : len < 0 || len > a.cap_u ? 1 : 0;
+            sh_seqs[s] = ChunkSeq{lo, hi - lo, len, bad};
+        }
+        if (tid == 0) sh_bad = 0;
+        __syncthreads();
+        if (a.paged) {
+            const int total = a.batch * a.max_pages;
+            for (int x = tid; x < total; x += kChunkPlanThreads) {
+                const int s = x / a.max_pages, p = x - s * a.max_pages;
+                const int id = __ldg(a.block_table + x);
+                if (p * a.page_size < sh_seqs[s].len && sh_seqs[s].n > 0 && sh_seqs[s].bad == 0 && (id < 0 || id >= a.n_pages))
+                    sh_bad = 1;
+            }
+            __syncthreads();
+            if (sh_bad) {  // some page is missing: which sequences lack one
+                for (int s = warp; s < a.batch; s += kChunkPlanThreads / 32) {
+                    bool ok = true;
+                    if (sh_seqs[s].n > 0 && sh_seqs[s].bad == 0)
+                        for (int p = lane; p * a.page_size < sh_seqs[s].len; p += 32) {
+                            const int id = __ldg(a.block_table + (long long)s * a.max_pages + p);
+                            ok = ok && id >= 0 && id < a.n_pages;
+                        }
+                    ok = __all_sync(FULL, ok);
+                    if (!ok && lane == 0) sh_seqs[s].bad = 2;  // TRI_DEV_BAD_PAGE
+                }
+                __syncthreads();
+            }
+        }
+        for (int s = tid; s < a.batch; s += kChunkPlanThreads)
+            if (sh_seqs[s].bad) record_status(a.status, sh_seqs[s].bad, (long long)s * a.n_kv);
+    } else {
+        const int s0 = blockIdx.x;
         const int lo = __ldg(a.cu + s0), hi = __ldg(a.cu + s0 + 1), len = __ldg(a.lens + s0);
         const long long cap = a.cap_u;
         int bad = 0;
@@ -157,9 +195,11 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
             sh_last = atomicAdd(&a.head->ticket, 1u) == gridDim.x - 1;
         }
     }
-    __syncthreads();
-    if (!sh_last) return;
-    __threadfence();
+    if (!alone) {
+        __syncthreads();
+        if (!sh_last) return;
+        __threadfence();
+    }
 
     // small plans are worked out in shared memory, larger ones in the workspace
     const ChunkSeq *seqs = a.batch <= kChunkPlanSeqs ? sh_seqs : a.seqs;
@@ -167,16 +207,20 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
     // blocks before each sequence; a bad range refuses every sequence (the ranges may overlap)
     bool range_ok = true;
     for (int s = tid; s < a.batch; s += kChunkPlanThreads) {
-        const int4 v = __ldcg(reinterpret_cast<const int4 *>(a.seqs + s));
-        if (a.batch <= kChunkPlanSeqs) sh_seqs[s] = ChunkSeq{v.x, v.y, v.z, v.w};
-        range_ok = range_ok && v.w != kDevBadRange;
+        if (!alone) {
+            const int4 v = __ldcg(reinterpret_cast<const int4 *>(a.seqs + s));
+            if (a.batch <= kChunkPlanSeqs) sh_seqs[s] = ChunkSeq{v.x, v.y, v.z, v.w};
+            range_ok = range_ok && v.w != kDevBadRange;
+        } else {
+            range_ok = range_ok && sh_seqs[s].bad != kDevBadRange;
+        }
     }
     range_ok = __syncthreads_and(range_ok);
     if (tid == 0) {
         sh_run = 0;
         sh_sum = 0;
         sh_max = 0;
-        a.head->ticket = 0;
+        if (!alone) a.head->ticket = 0;
     }
     __syncthreads();
     const int G = a.group, tpb = kChunkRows / G;
@@ -223,7 +267,7 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
         x.nsplit = 1;
         x.split = 0;
         x.slot = 0;
-        x.group = 0;
+        x.unused = 0;
         x.pair = 0;
         return x;
     };
@@ -246,53 +290,57 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
         }
     }
     __syncthreads();
-    // the longest split: warp w weighs one candidate, a share of an SM's even part of the work. The
+    // the longest split: the warps weigh candidates, each a share of an SM's even part of the work. The
     // time of a candidate is at most rounds * longest and at most even part + longest (both bounds
     // of handing items out longest first); the smaller of them counts.
     {
-        const long long even = (sh_sum * LH + a.sm_count - 1) / a.sm_count;
-        // even, 2/3, 1/2, 2/5, 1/3, 1/4, 1/6 of it; warp 0 does not split
-        const int num[8] = {1, 1, 2, 1, 2, 1, 1, 1}, den[8] = {1, 1, 3, 2, 5, 3, 4, 6};
-        const long long want = (even * num[warp] + den[warp] - 1) / den[warp];
-        const int chunk = warp == 0 ? max(1, sh_max) : (int)max(2LL, min((long long)max(1, sh_max), want));
-        long long items = 0, work = 0;
-        int longest = 0, slots = 0, lines = 0, merge_rows = 0;
-        for (int e = lane; e < n_blocks; e += 32) {
-            const int t = tiles[e];
-            int ns = max(1, (t + chunk - 1) / chunk);
-            const int per = (t + ns - 1) / ns;
-            if (t > 0) ns = (t + per - 1) / per;
-            items += ns;
-            lines += ns;
-            work += t + (long long)ns * kChunkItemCost;
-            longest = max(longest, per);
-            if (ns > 1) {
-                slots += ns;
-                merge_rows = max(merge_rows, min(tpb, a.n_tokens));
+        const float per_sm = 1.f / (float)a.sm_count, even = (float)sh_sum * (float)LH * per_sm;
+        // the first candidate does not split
+        __shared__ float share[kChunkCandidates];
+        if (tid < kChunkCandidates)  // 1.6, 1.3, 1.15, 1.07, 1, and 1 / n of it down to 1/6
+            share[tid] = tid < 5 ? 1.f + (tid == 1 ? .6f : tid == 2 ? .3f : tid == 3 ? .15f : .07f) : 2.f / (float)(tid - 3);
+        __syncthreads();
+#pragma unroll 1
+        for (int cand = warp; cand < kChunkCandidates; cand += kChunkPlanThreads / 32) {
+            const float want = ceilf(even * share[cand]);
+            const int chunk = cand == 0 ? max(1, sh_max) : max(2, (int)fminf((float)max(1, sh_max), want));
+            int items = 0, work = 0, longest = 0, slots = 0, merge_rows = 0;
+#pragma unroll 1
+            for (int e = lane; e < n_blocks; e += 32) {
+                const int t = tiles[e];
+                int ns = max(1, (t + chunk - 1) / chunk);
+                const int per = (t + ns - 1) / ns;
+                if (t > 0) ns = (t + per - 1) / per;
+                items += ns;
+                work += t + ns * kChunkItemCost;
+                longest = max(longest, per);
+                if (ns > 1) {
+                    slots += ns;
+                    merge_rows = max(merge_rows, min(tpb, a.n_tokens));
+                }
+            }
+            items = __reduce_add_sync(FULL, items);
+            work = __reduce_add_sync(FULL, work);
+            longest = __reduce_max_sync(FULL, longest);
+            slots = __reduce_add_sync(FULL, slots);
+            merge_rows = __reduce_max_sync(FULL, merge_rows);
+            if (lane == 0) {
+                const float one = (float)(longest + kChunkItemCost);
+                float cost = fminf(ceilf((float)items * (float)LH * per_sm) * one, (float)work * (float)LH * per_sm + one);
+                if (slots > 0) cost += (float)(kChunkMergeCost + kChunkMergeRows * merge_rows / tpb);
+                if ((long long)slots * LH > a.max_slots || items > a.max_entries) cost = 3e38f;
+                est[cand] = cost;
+                est_chunk[cand] = chunk;
             }
         }
-        for (int o = 16; o; o >>= 1) {
-            items += __shfl_xor_sync(FULL, items, o);
-            work += __shfl_xor_sync(FULL, work, o);
-            longest = max(longest, __shfl_xor_sync(FULL, longest, o));
-            slots += __shfl_xor_sync(FULL, slots, o);
-            lines += __shfl_xor_sync(FULL, lines, o);
-        }
-        if (lane == 0) {
-            const long long rounds = (items * LH + a.sm_count - 1) / a.sm_count;
-            const long long one = longest + kChunkItemCost;
-            long long cost = min(rounds * one, (work * LH + a.sm_count - 1) / a.sm_count + one);
-            if (slots > 0) cost += kChunkMergeCost + kChunkMergeRows * merge_rows / tpb;
-            if ((long long)slots * LH > a.max_slots || lines > a.max_entries) cost = 1LL << 60;
-            est[warp] = cost;
-            est_chunk[warp] = chunk;
-        }
     }
-    for (int i = tid; i < kChunkSortBins; i += kChunkPlanThreads) hist[i] = 0;
+    // (only the bins of lengths up to the longest are used)
+    const int bin0 = (kChunkSortBins - 1 - min(sh_max, kChunkSortBins - 1)) & ~31;
+    for (int i = bin0 + tid; i < kChunkSortBins; i += kChunkPlanThreads) hist[i] = 0;
     __syncthreads();
     if (tid == 0) {
         int best = 0;
-        for (int w = 1; w < 8; ++w)
+        for (int w = 1; w < kChunkCandidates; ++w)
             if (est[w] < est[best]) best = w;
         sh_chunk = est_chunk[best];
         sh_slots = 0;
@@ -312,7 +360,7 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
     __syncthreads();
     if (warp == 0) {  // exclusive prefix sums of the bins
         int run = 0;
-        for (int i0 = 0; i0 < kChunkSortBins; i0 += 32) {
+        for (int i0 = bin0; i0 < kChunkSortBins; i0 += 32) {
             const int x = hist[i0 + lane];
             int inc = x;
             for (int o = 1; o < 32; o <<= 1) {
@@ -335,7 +383,7 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
         x.nsplit = ns;
         if (ns > 1) {
             x.slot = atomicAdd(&sh_slots, ns);
-            x.group = atomicAdd(&sh_groups, 1);
+            a.merges[atomicAdd(&sh_groups, 1)] = x;
         }
         for (int k = 0; k < ns; ++k) {
             x.split = k;
@@ -346,8 +394,10 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
         }
     }
     __syncthreads();
-    for (int i = tid; i < 2 * sh_groups * LH; i += kChunkPlanThreads) a.counters[i] = 0;
-    if (tid == 0) a.head->n_entries = sh_entries;
+    if (tid == 0) {
+        a.head->n_entries = sh_entries;
+        a.head->n_groups = sh_groups;
+    }
 }
 
 // ---------------------------------------------------------------------------------
@@ -524,9 +574,9 @@ __host__ __device__ inline ChunkSmem chunk_smem(int D) {
     L.ring = 2u * (unsigned)D * 256u;               // two query tiles of 128 rows
     L.ml = L.ring + NST * (unsigned)D * 256u;  // a paired item's second (m, l) of each row
     L.bars = L.ml + 128u * 8u;
-    // full, empty [stages each], q full and empty, S, P, most of P and O full [2 each], done, parts written and merge
-    // decided [2 each], exchange full and free, turns [2], TMEM address, abort, merge[2]
-    L.total = L.bars + (2u * NST + 19u) * 8u + 32u + 1024u;  // + alignment slack
+    // full, empty [stages each], q full and empty, S, P, most of P and O full [2 each], done, exchange full and free,
+    // turns [2], TMEM address, abort
+    L.total = L.bars + (2u * NST + 15u) * 8u + 32u + 1024u;  // + alignment slack
     return L;
 }
 
@@ -666,68 +716,6 @@ __device__ __forceinline__ void chunk_softmax_tile(uint32_t ts, uint32_t to, flo
     tmem_wait_st();
 }
 
-// Join the parts of a block's row tile in the order of the keys: `first` + 2 k for k < nsplit. Each thread
-// takes one row (of the rows rounded up to a power of two) and every (128 / rows)-th piece of 4 dims, 4 pieces
-// of 4 parts in flight.
-template <int D>
-__device__ __forceinline__ void chunk_merge(const ChunkArgs &a, long long first, int nsplit, int nv, int t, int G, int r0,
-                                            int lr, int g, int tok0) {
-    const float NEG_INF = __int_as_float(0xff800000);
-    const int shift = 32 - __clz(nv - 1);       // nv >= 1: rows rounded up to 2^shift
-    const int rr = t & ((1 << shift) - 1), step = 128 >> shift;
-    if (rr >= nv) return;
-    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + first * 128 + rr;
-    float M = NEG_INF;
-#pragma unroll 4
-    for (int k = 0; k < nsplit; ++k) M = fmaxf(M, __ldcg(ml + k * 256).x);
-    float L = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < nsplit; ++k) {
-        const float2 x = __ldcg(ml + k * 256);
-        if (x.y != 0.f) L += x.y * ex2_approx(x.x - M);  // a part that sees no key of the row weighs nothing
-    }
-    const float li = L == 0.f ? 0.f : 1.f / L;
-    const int row = r0 + rr, rh = g * G + row % G;
-    const long long tok = tok0 + row / G;
-    const float4 *part = reinterpret_cast<const float4 *>(a.part) + (first * (D / 4)) * 128 + rr;
-    uint16_t *out = a.out + lr * a.o_l + tok * a.o_t + rh * a.o_h;
-    for (int c0 = t >> shift; c0 < D / 4; c0 += 4 * step) {
-        float4 A[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) A[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < nsplit; ++k) {
-            const float2 x = __ldcg(ml + k * 256);
-            const float w = x.y == 0.f ? 0.f : ex2_approx(x.x - M);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int c = c0 + i * step;
-                if (c < D / 4) {
-                    const float4 v = __ldcg(part + ((long long)k * 2 * (D / 4) + c) * 128);
-                    if (x.y != 0.f) {
-                        A[i].x = fmaf(v.x, w, A[i].x);
-                        A[i].y = fmaf(v.y, w, A[i].y);
-                        A[i].z = fmaf(v.z, w, A[i].z);
-                        A[i].w = fmaf(v.w, w, A[i].w);
-                    }
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = c0 + i * step;
-            if (c < D / 4) {
-                uint2 w;
-                w.x = pack_bf16(A[i].x * li, A[i].y * li);
-                w.y = pack_bf16(A[i].z * li, A[i].w * li);
-                *reinterpret_cast<uint2 *>(out + 4 * c) = w;
-            }
-        }
-    }
-    if (a.lse && t < (1 << shift))
-        a.lse[((long long)lr * a.n_tokens + tok) * (a.n_kv * G) + rh] = L == 0.f ? NEG_INF : (M + log2f(L)) * 0.6931471805599453f;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     tri_chunk_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -751,15 +739,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint64_t *pmost = pfull + 2;    // [2]
     uint64_t *ofull = pmost + 2;    // [2]
     uint64_t *done = ofull + 2;
-    uint64_t *parts = done + 1;     // [2]
-    uint64_t *decided = parts + 2;  // [2]
-    uint64_t *xfull = decided + 2;
+    uint64_t *xfull = done + 1;
     uint64_t *xfree = xfull + 1;
     uint64_t *turn = xfree + 1;     // [2]
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(turn + 2);
     float2 *ml_x = reinterpret_cast<float2 *>(smem + Ly.ml);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    volatile int *merge_flag = abort_flag + 1;        // [2]
 
     const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
@@ -774,8 +759,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             mbar_init(pfull + i, 4);  // the warpgroup's warps
             mbar_init(pmost + i, 4);
             mbar_init(ofull + i, 1);
-            mbar_init(parts + i, 4);
-            mbar_init(decided + i, 1);
             mbar_init(turn + i, 1);
         }
         mbar_init(done, 2);
@@ -798,11 +781,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     const int G = a.group, LH = a.n_layers * a.n_kv;
-    const long long n_items = (long long)a.head->n_entries * LH;
+    const unsigned n_items = (unsigned)a.head->n_entries * (unsigned)LH;  // below 2^31
     // this CTA's item of round r: forth in even rounds, back in odd ones
     auto item_of = [&](int r) {
         const int pos = (r & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
-        return (long long)r * gridDim.x + pos;
+        return (unsigned)r * gridDim.x + (unsigned)pos;
     };
     auto fail = [&](const ChunkEntry &e, int lh) {
         record_status(a.status, kDevTimeout, ((long long)(lh / a.n_kv) * a.batch + e.s) * a.n_kv + lh % a.n_kv);
@@ -817,7 +800,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         int k = 0, nq = 0;      // ring fills so far, query tiles loaded so far
         bool ok = true;
         for (int r = 0; ok && !*abort_flag; ++r) {
-            const long long it = item_of(r);
+            const unsigned it = item_of(r);
             if (it >= n_items) break;
             const ChunkEntry e = a.entries[it / LH];
             const int lh = (int)(it % LH), lr = lh / a.n_kv, g = lh % a.n_kv;
@@ -911,7 +894,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             at.step();
         };
         for (int r = 0; ok && !*abort_flag; ++r) {
-            const long long it = item_of(r);
+            const unsigned it = item_of(r);
             if (it >= n_items) break;
             const ChunkEntry e = a.entries[it / LH];
             // (values that the compiler shall know to be the same in every lane go through a shuffle)
@@ -1025,11 +1008,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int row = (warp & 3) * 32 + lane;          // TMEM lane
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + 128u * q, to = tmem + lanes + 256u + (uint32_t)(D * q);
-        const int wg_tid = tid & 127;
-        unsigned ns = 0, no = 0, nm = 0, nx = 0;  // S tiles, items, items in parts, paired items so far
+        unsigned ns = 0, no = 0, nx = 0;  // S tiles, items, paired items so far
         bool ok = true;
         for (int r = 0; ok && !*abort_flag; ++r) {
-            const long long it = item_of(r);
+            const unsigned it = item_of(r);
             if (it >= n_items) break;
             const ChunkEntry *ep = a.entries + it / LH;
             const int lh = (int)(it % LH);
@@ -1199,31 +1181,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 __syncwarp();
             }
-            if (nsplit > 1) {
-                // the last part of the block to arrive merges them all, in the order of the keys
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(parts + q);
-                ok = __all_sync(FULL, mbar_wait_bounded(parts + q, nm & 1u, a.wait_tries));
-                if (ok && wg_tid == 0) {
-                    const long long grp = ((long long)ec.w * LH + lh) * 2 + tile;
-                    merge_flag[q] = atomicAdd(a.counters + grp, 1u) == (unsigned)nsplit - 1;
-                    __threadfence();
-                    mbar_arrive(decided + q);
-                }
-                __syncwarp();
-                ok = ok && __all_sync(FULL, mbar_wait_bounded(decided + q, nm & 1u, a.wait_tries));
-                if (!ok) {
-                    if (lane == 0) fail(*ep, lh);
-                    break;
-                }
-                ++nm;
-                // the flag is written again only after every warp has arrived with its next part
-                if (merge_flag[q]) {
-                    const long long first = ((long long)ec.z * LH + (long long)lh * nsplit) * 2 + tile;
-                    chunk_merge<D>(a, first, nsplit, min(128, rows), wg_tid, G, r0, lr, g, ea.y);
-                }
-            }
         }
     }
     tc_fence_before();
@@ -1231,6 +1188,63 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    }
+}
+
+// Joins the parts of every block that was split, in the order of the keys: out = sum_k 2^(m_k - M) acc_k / sum_k
+// 2^(m_k - M) l_k. A programmatic dependent of the attention kernel. In a launch of its own because the last
+// CTA of a block did it far slower: one CTA per block against all of them, and code that no CTA had fetched
+// yet in the middle of the kernel (18 parts of 8 rows took 18 us).
+constexpr int kChunkMergeThreads = 256;
+constexpr int kChunkMergeShare = 8;  // CTAs that share the rows of a block's query tile
+template <int D>
+__global__ void __launch_bounds__(kChunkMergeThreads) tri_chunk_merge_kernel(const ChunkArgs a) {
+    const float NEG_INF = __int_as_float(0xff800000);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int G = a.group, LH = a.n_layers * a.n_kv;
+    const int units = a.head->n_groups * LH * 2 * kChunkMergeShare;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        const int share = u % kChunkMergeShare, tile = u / kChunkMergeShare % 2;
+        const int lh = u / (2 * kChunkMergeShare) % LH, grp = u / (2 * kChunkMergeShare) / LH;
+        const ChunkEntry e = a.merges[grp];
+        const int nv = min(128, e.ntok * G - 128 * tile);
+        if (nv <= 0) continue;
+        const int lr = lh / a.n_kv, g = lh % a.n_kv;
+        const long long first = ((long long)e.slot * LH + (long long)lh * e.nsplit) * 2 + tile;
+        const float2 *ml0 = reinterpret_cast<const float2 *>(a.part_ml) + first * 128;
+        const float4 *part0 = reinterpret_cast<const float4 *>(a.part) + first * (D / 4) * 128;
+        const int shift = 32 - __clz(nv - 1);  // rows rounded up to a power of two, so that neighbours read neighbours
+        for (int x = share * kChunkMergeThreads + threadIdx.x; x < (D / 4) << shift; x += kChunkMergeShare * kChunkMergeThreads) {
+            const int rr = x & ((1 << shift) - 1), c = x >> shift;
+            if (rr >= nv) continue;
+            float M = NEG_INF, L = 0.f;
+            float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int k = 0; k < e.nsplit; ++k) M = fmaxf(M, ml0[k * 256 + rr].x);
+#pragma unroll 8
+            for (int k = 0; k < e.nsplit; ++k) {
+                const float2 ml = ml0[k * 256 + rr];
+                const float4 v = part0[((long long)k * 2 * (D / 4) + c) * 128 + rr];
+                if (ml.y != 0.f) {  // a part that sees no key of the row weighs nothing
+                    const float w = ex2_approx(ml.x - M);
+                    L = fmaf(ml.y, w, L);
+                    A.x = fmaf(v.x, w, A.x);
+                    A.y = fmaf(v.y, w, A.y);
+                    A.z = fmaf(v.z, w, A.z);
+                    A.w = fmaf(v.w, w, A.w);
+                }
+            }
+            const float li = L == 0.f ? 0.f : 1.f / L;
+            const int row = 128 * tile + rr, rh = g * G + row % G;
+            const long long tok = e.tok0 + row / G;
+            uint2 w;
+            w.x = pack_bf16(A.x * li, A.y * li);
+            w.y = pack_bf16(A.z * li, A.w * li);
+            *reinterpret_cast<uint2 *>(a.out + lr * a.o_l + tok * a.o_t + rh * a.o_h + 4 * c) = w;
+            if (c == 0 && a.lse)
+                a.lse[((long long)lr * a.n_tokens + tok) * (a.n_kv * G) + rh] =
+                    L == 0.f ? NEG_INF : (M + log2f(L)) * 0.6931471805599453f;
+        }
     }
 }
 
