@@ -1206,7 +1206,7 @@ const void *rope_kernel_of(int layout) {
 // eight a SM while there are that many tokens.
 tri_status launch_rope(tri_ctx *c, tri::RopeArgs &a, int D, int n_layers, bool append, void *stream) {
     a.units = (a.q.heads + a.k.heads + a.v.heads) * (D / 16);
-    const long long want = (tri::kRopeThreads * tri::kRopeBatch + a.units - 1) / a.units;
+    const long long want = tri::kRopeThreads * tri::kRopeBatch / a.units;
     const long long room = (long long)a.n_tokens * n_layers / (8LL * c->sm_count);
     a.tpc = (int)std::max<long long>(1, std::min<long long>(tri::kRopeMaxTokens, std::min(want, room)));
     a.units_magic = a.units > 1 ? (unsigned)(((1ull << 32) + a.units - 1) / a.units) : 0u;

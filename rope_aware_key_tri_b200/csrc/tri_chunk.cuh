@@ -1219,9 +1219,9 @@ __global__ void __launch_bounds__(kChunkMergeThreads) tri_chunk_merge_kernel(con
             if (rr >= nv) continue;
             float M = NEG_INF, L = 0.f;
             float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 16
             for (int k = 0; k < e.nsplit; ++k) M = fmaxf(M, ml0[k * 256 + rr].x);
-#pragma unroll 8
+#pragma unroll 16
             for (int k = 0; k < e.nsplit; ++k) {
                 const float2 ml = ml0[k * 256 + rr];
                 const float4 v = part0[((long long)k * 2 * (D / 4) + c) * 128 + rr];

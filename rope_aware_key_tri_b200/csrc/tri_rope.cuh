@@ -27,8 +27,8 @@
 
 namespace tri {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 2;      // units a thread has in flight
+constexpr int kRopeThreads = 128;
+constexpr int kRopeBatch = 3;      // units a thread has in flight
 constexpr int kRopeMaxTokens = 32; // tokens of a CTA, at most
 constexpr int kDevBadRange = 6;    // TRI_DEV_BAD_RANGE
 
@@ -77,33 +77,38 @@ struct TokenPlace {
     int seq, slot, page;
 };
 
-// The sequence of token t by counting the starts at or below it (32 at a time: one load for up to 32
+// The sequence of token t by counting the ends at or below it (32 at a time: one load for up to 32
 // sequences, against log2(batch) dependent ones of a bisection), with the check that the starts
 // ascend within [0, n_tokens]; if they do not, no token has a place. Then the sequence's verdict:
 // all its new slots below the capacity and all their pages allocated, so that a refused sequence
 // is refused by every CTA alike.
 __device__ __forceinline__ TokenPlace token_place(const RopeArgs &a, int t, int lane, int *bad_code) {
     constexpr unsigned FULL = 0xffffffffu;
-    int below = 0;
+    int s = -1, t0 = 0, t1 = 0, len = 0;
     bool sane = true;
     for (int i0 = 0; i0 < a.batch; i0 += 32) {
         const int i = i0 + lane;
-        int lo = 0, hi = 0;
+        int lo = 0, hi = 0, ln = 0;
         if (i < a.batch) {
             lo = __ldg(a.cu + i);
             hi = __ldg(a.cu + i + 1);
+            ln = a.lens[i];  // a plain load: lens_out may be lens
         }
         sane = sane && lo >= 0 && lo <= hi && hi <= a.n_tokens;
-        below += __popc(__ballot_sync(FULL, i < a.batch && hi <= t));
+        const unsigned past = __ballot_sync(FULL, i < a.batch && hi <= t), all = __ballot_sync(FULL, i < a.batch);
+        if (s < 0 && past != all) {
+            const int src = __popc(past);
+            s = i0 + src;
+            t0 = __shfl_sync(FULL, lo, src);
+            t1 = __shfl_sync(FULL, hi, src);
+            len = __shfl_sync(FULL, ln, src);
+        }
     }
     *bad_code = 0;
     TokenPlace r{-1, 0, 0};
-    if (!__all_sync(FULL, sane)) return r;
-    const int s = below;
-    if (s >= a.batch) return r;  // behind the last sequence
-    const int t0 = __ldg(a.cu + s), n = __ldg(a.cu + s + 1) - t0;
-    if (t < t0) return r;        // before the first
-    const int len = a.lens[s];   // a plain load: lens_out may be lens
+    // not ascending, or behind the last sequence, or before the first
+    if (!__all_sync(FULL, sane) || s < 0 || t < t0) return r;
+    const int n = t1 - t0;
     const long long cap = a.page_size ? (long long)a.page_size * a.max_pages : a.cap;
     if (len < 0 || (long long)len + n > cap) {
         *bad_code = 1;           // TRI_DEV_LEN_GT_CAP
@@ -113,18 +118,16 @@ __device__ __forceinline__ TokenPlace token_place(const RopeArgs &a, int t, int 
     if (a.page_size) {
         const int p0 = len / a.page_size, p1 = (len + n - 1) / a.page_size;
         const int32_t *row = a.block_table + (long long)s * a.max_pages;
-        bool ok = true;
-        for (int p = p0 + lane; p <= p1; p += 32) {
-            const int id = __ldg(row + p);
-            ok = ok && id >= 0 && id < a.n_pages;
-        }
-        if (!__all_sync(FULL, ok)) {
+        const int slot = len + (t - t0);
+        r.page = __ldg(row + slot / a.page_size);
+        int bad = 0;
+#pragma unroll 4
+        for (int p = p0 + lane; p <= p1; p += 32) bad |= (unsigned)__ldg(row + p) >= (unsigned)a.n_pages;
+        if (__any_sync(FULL, bad)) {
             *bad_code = 2;       // TRI_DEV_BAD_PAGE
             r.seq = s;
             return r;
         }
-        const int slot = len + (t - t0);
-        r.page = __ldg(row + slot / a.page_size);
         r.slot = slot % a.page_size;
     } else {
         r.page = s;
