@@ -564,6 +564,10 @@ __device__ __forceinline__ float2 exp2_pair(float2 x) {
 
 constexpr int kChunkEmu128 = 1, kChunkEmu64 = 0;
 
+// Heads of 64 leave 128 columns of tensor memory free: P has columns of its own there, so that the next S is
+// computed while the warpgroup still exponentiates this one (at head 128 P lies over S).
+__host__ __device__ constexpr bool chunk_apart(int D) { return D == 64; }
+
 struct ChunkSmem {
     unsigned q, ring, ml, bars, total;
 };
@@ -574,9 +578,10 @@ __host__ __device__ inline ChunkSmem chunk_smem(int D) {
     L.ring = 2u * (unsigned)D * 256u;               // two query tiles of 128 rows
     L.ml = L.ring + NST * (unsigned)D * 256u;  // a paired item's second (m, l) of each row
     L.bars = L.ml + 128u * 8u;
-    // full, empty [stages each], q full and empty, S, P, most of P and O full [2 each], done, exchange full and free,
+    // full, empty [stages each], q full and empty, S, P, most of P and O full [2 each], done, S free and
+    // P V done [2 each], exchange full and free,
     // turns [2], TMEM address, abort
-    L.total = L.bars + (2u * NST + 15u) * 8u + 32u + 1024u;  // + alignment slack
+    L.total = L.bars + (2u * NST + 19u) * 8u + 32u + 1024u;  // + alignment slack
     return L;
 }
 
@@ -628,8 +633,9 @@ __device__ __forceinline__ void chunk_row_again(const ChunkArgs &a, int s, int l
 // The hardware exponential takes 8 clocks a warp, 1024 for the tile; `kEmu` of every 8 pairs are
 // evaluated on the FMA pipe instead, about where the two pipes finish together.
 template <int D>
-__device__ __forceinline__ void chunk_softmax_tile(uint32_t ts, uint32_t to, float c, bool cut, int left, bool fresh,
-                                                   float &m, float &l, int lane, uint64_t *most) {
+__device__ __forceinline__ bool chunk_softmax_tile(uint32_t ts, uint32_t tp, uint32_t to, float c, bool cut, int left,
+                                                   bool fresh, float &m, float &l, int lane, uint64_t *most,
+                                                   uint64_t *sfree, uint64_t *pv, unsigned pv_parity, int tries) {
     constexpr unsigned FULL = 0xffffffffu;
     constexpr int kEmu = D == 128 ? kChunkEmu128 : kChunkEmu64;
     const float NEG_INF = __int_as_float(0xff800000);
@@ -658,6 +664,11 @@ __device__ __forceinline__ void chunk_softmax_tile(uint32_t ts, uint32_t to, flo
     tmem_wait32(s1);
     tmem_after32(s2);
     tmem_after32(s3);
+    if (chunk_apart(D)) {  // the next S may come
+        tc_fence_before();
+        __syncwarp();
+        arrive_if(sfree, lane == 0);
+    }
     top(s1, 32);
     top(s2, 64);
     top(s3, 96);
@@ -665,7 +676,9 @@ __device__ __forceinline__ void chunk_softmax_tile(uint32_t ts, uint32_t to, flo
     if (fresh) {
         m = mx;
     } else if (__any_sync(FULL, mx != NEG_INF && !((mx - m) * c <= 8.f))) {
-        // P V of the tiles before is complete: O is this warpgroup's to rescale
+        // once P V of the tiles before is complete, O is this warpgroup's to rescale
+        if (chunk_apart(D) && !__all_sync(FULL, mbar_wait_bounded(pv, pv_parity, tries))) return false;
+        tc_fence_after();
         const float mn = max3nan(m, mx, mx);
         const float f = m == mn ? 1.f : ex2_approx((m - mn) * c);
         m = mn;
@@ -698,11 +711,15 @@ __device__ __forceinline__ void chunk_softmax_tile(uint32_t ts, uint32_t to, flo
         }
     };
     weights(s0, 0, 32);
-    tmem_st16(ts, p);
+    if (chunk_apart(D) && !fresh) {  // the P before has been read
+        if (!__all_sync(FULL, mbar_wait_bounded(pv, pv_parity, tries))) return false;
+        tc_fence_after();
+    }
+    tmem_st16(tp, p);
     weights(s1, 0, 32);
-    tmem_st16(ts + 16u, p);
+    tmem_st16(tp + 16u, p);
     weights(s2, 0, 32);
-    tmem_st16(ts + 32u, p);
+    tmem_st16(tp + 32u, p);
     // the first 96 keys' weights are handed over once their stores, by now under way for a while, are done,
     // so that most of P V runs during the rest
     weights(s3, 0, 16);
@@ -711,9 +728,10 @@ __device__ __forceinline__ void chunk_softmax_tile(uint32_t ts, uint32_t to, flo
     __syncwarp();
     arrive_if(most, lane == 0);
     weights(s3, 16, 32);
-    tmem_st16(ts + 48u, p);
+    tmem_st16(tp + 48u, p);
     l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
     tmem_wait_st();
+    return true;
 }
 
 template <int D>
@@ -739,7 +757,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint64_t *pmost = pfull + 2;    // [2]
     uint64_t *ofull = pmost + 2;    // [2]
     uint64_t *done = ofull + 2;
-    uint64_t *xfull = done + 1;
+    uint64_t *sfree = done + 1;     // [2] (heads of 64)
+    uint64_t *pv = sfree + 2;       // [2] (heads of 64)
+    uint64_t *xfull = pv + 2;
     uint64_t *xfree = xfull + 1;
     uint64_t *turn = xfree + 1;     // [2]
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(turn + 2);
@@ -759,6 +779,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             mbar_init(pfull + i, 4);  // the warpgroup's warps
             mbar_init(pmost + i, 4);
             mbar_init(ofull + i, 1);
+            mbar_init(sfree + i, 4);
+            mbar_init(pv + i, 1);
             mbar_init(turn + i, 1);
         }
         mbar_init(done, 2);
@@ -878,6 +900,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t q_low = desc_low(smem_u32(smem + Ly.q), 16u), k_low = desc_low(smem_u32(smem + Ly.ring), 16u);
         const uint32_t v_low = desc_low(smem_u32(smem + Ly.ring), kChunkBytes);
         const uint32_t sd = tmem + 128u * q, od = tmem + 256u + (uint32_t)(D * q);
+        const uint32_t pd = chunk_apart(D) ? tmem + 384u + 64u * q : sd;
         const uint32_t lead_lane = elect_one();
         ChunkRing<NST> at;            // the next tile
         unsigned nq = 0, np = 0;      // items, P tiles so far
@@ -961,32 +984,40 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     }
                     const uint32_t vl = __shfl_sync(FULL, v_low + (unsigned)av.stage * (kTileBytes >> 4), 0);
                     const uint32_t bl = __shfl_sync(FULL, k_low + (unsigned)at.stage * (kTileBytes >> 4), 0);
-                    ok = (!more || wait(full + at.stage, at.phase)) && wait(pmost + q, np);
+                    ok = !more || wait(full + at.stage, at.phase);
+                    if (chunk_apart(D) && more && ok) {
+                        ok = wait(sfree + q, np);
+                        tc_fence_after();
+                        mma_s(bl, lead_lane && ok);
+                        commit_if(empty + at.stage, lead_lane && ok);
+                        commit_if(qempty, lead_lane && ok && i + lead == end);
+                    }
+                    ok = ok && wait(pmost + q, np);
                     // the two warps take turns: MMAs of both at once would share the tensor core, end together
                     // and leave it idle while both warpgroups exponentiate
-                    if (ok && (q == 1 || owed)) ok = wait(turn + (q ^ 1), nt++);
+                    if (!chunk_apart(D) && ok && (q == 1 || owed)) ok = wait(turn + (q ^ 1), nt++);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < 6; ++ks)  // 16 keys: 16 rows of 128 bytes of each chunk
-                        chunk_mma_ts(od, sd + 8u * ks, vl + ks * 128u, id_o, (i >= lead || ks > 0), lead_lane);
+                        chunk_mma_ts(od, pd + 8u * ks, vl + ks * 128u, id_o, (i >= lead || ks > 0), lead_lane);
                     ok = wait(pfull + q, np);
                     ++np;
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int ks = 6; ks < 8; ++ks) chunk_mma_ts(od, sd + 8u * ks, vl + ks * 128u, id_o, 1, lead_lane);
-                    if (more) {
+                    for (int ks = 6; ks < 8; ++ks) chunk_mma_ts(od, pd + 8u * ks, vl + ks * 128u, id_o, 1, lead_lane);
+                    if (chunk_apart(D)) {
+                        commit_if(pv + q, lead_lane);
+                    } else if (more) {
                         mma_s(bl, lead_lane);
-                        commit_if(empty + av.stage, lead_lane);
                         commit_if(empty + at.stage, lead_lane);
                         commit_if(qempty, lead_lane && i + lead == end);
-                    } else {
-                        commit_if(ofull + q, lead_lane);
-                        commit_if(empty + av.stage, lead_lane);
                     }
-                    owed = q == 0 && (pair ? i + 1 < n : both);
-                    arrive_if(turn + q, lane == 0 && (q == 1 || owed));
+                    commit_if(empty + av.stage, lead_lane);
+                    commit_if(ofull + q, lead_lane && !more);
+                    owed = !chunk_apart(D) && q == 0 && (pair ? i + 1 < n : both);
+                    arrive_if(turn + q, lane == 0 && !chunk_apart(D) && (q == 1 || owed));
                     if (more) at.step();
                 }
             }
@@ -1008,6 +1039,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int row = (warp & 3) * 32 + lane;          // TMEM lane
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + 128u * q, to = tmem + lanes + 256u + (uint32_t)(D * q);
+        const uint32_t tp = chunk_apart(D) ? tmem + lanes + 384u + 64u * q : ts;
         unsigned ns = 0, no = 0, nx = 0;  // S tiles, items, paired items so far
         bool ok = true;
         for (int r = 0; ok && !*abort_flag; ++r) {
@@ -1036,9 +1068,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     if (work) {
                         tc_fence_after();
                         const int key0 = (e.kt0 + i) * 128;
-                        chunk_softmax_tile<D>(ts, to, a.c, key0 + 128 > sure, limit - key0, i < step, m, l, lane, pmost + q);
+                        ok = chunk_softmax_tile<D>(ts, tp, to, a.c, key0 + 128 > sure, limit - key0, i < step, m, l, lane,
+                                                   pmost + q, sfree + q, pv + q, ns & 1u, a.wait_tries);
+                        if (!ok) break;
                         tc_fence_before();
                     } else {
+                        if (chunk_apart(D)) {
+                            arrive_if(sfree + q, lane == 0);
+                            // no earlier than a warp with rows could: this arrival belongs to this tile's phase
+                            if (i >= step) ok = __all_sync(FULL, mbar_wait_bounded(pv + q, ns & 1u, a.wait_tries));
+                            if (!ok) break;
+                        }
                         arrive_if(pmost + q, lane == 0);
                     }
                     __syncwarp();
