@@ -405,14 +405,14 @@ TRI_API tri_status tri_append_chunk(tri_ctx *ctx, const tri_kv *kv, const tri_ro
  * accumulators are fp32; the weights are rounded to bf16 for the tensor cores (2^-9 each), the result once more.
  * Tokens outside every range are left unwritten; so are those of a refused sequence (TRI_DEV_LEN_GT_CAP,
  * TRI_DEV_BAD_PAGE; TRI_DEV_BAD_RANGE refuses all). A wait that ran out (TRI_DEV_TIMEOUT) leaves the result of
- * that call incomplete. Two launches on `stream` (a plan, and the attention as its programmatic dependent). The
- * result does not depend on the order in which parts finish.
+ * that call incomplete. Three launches on `stream` (a plan, the attention and the join of its parts, each a
+ * programmatic dependent of the one before). The result does not depend on the order in which parts finish.
  * Workspace of the context, allocated when a call needs more than any before (make the first call of the largest
  * shape before a capture; later growth leaves what a captured graph uses in place): about 4 * SMs * 256 *
- * (head_dim + 2) * 4 bytes (79 MB at head_dim 128), and 56 bytes per 256 query rows and sequence. The attention
+ * (head_dim + 2) * 4 bytes (79 MB at head_dim 128), and about 70 bytes per sequence and per 256 query rows. The attention
  * holds the whole tensor memory of every SM: do not run it beside other kernels that allocate tensor memory (see
- * tri_set_offset_combine). Limits: n_layers * pages (or batch) * n_kv_heads * page size (or cap) below 2^31. Needs
- * the statistics loaded. Errors: TRI_EINVAL, TRI_ESTATE, TRI_EUNSUPPORTED, TRI_ENOMEM, TRI_ECUDA.
+ * tri_set_offset_combine). Limits: n_layers * pages (or batch) * n_kv_heads * page size (or cap) below 2^31, and
+ * (n_tokens * group / 256 + batch) * capacity / 128 below 2^29. Needs the statistics loaded. Errors: TRI_EINVAL, TRI_ESTATE, TRI_EUNSUPPORTED, TRI_ENOMEM, TRI_ECUDA.
  */
 TRI_API tri_status tri_chunk_attention(tri_ctx *ctx, const tri_kv *kv, const tri_rows *q, const int32_t *cu_q,
                                        int n_tokens, double scale, int causal, const tri_rows *out, float *lse,
@@ -519,8 +519,8 @@ TRI_API tri_status tri_set_offset_combine(tri_ctx *ctx, int combine);
  */
 TRI_API tri_status tri_set_score_engine(tri_ctx *ctx, int engine);
 
-/* Tracing: tri_prune, tri_prune_noalloc, tri_score, tri_calibrate_estimate and tri_append each
- * mark their host-side span (argument checks and launches) with an NVTX range in the domain
+/* Tracing: tri_prune, tri_prune_noalloc, tri_score, tri_calibrate_estimate, tri_append, tri_rope, tri_append_chunk and
+ * tri_chunk_attention each mark their host-side span (argument checks and launches) with an NVTX range in the domain
  * "tri"; the max-over-offsets mode adds one range per chunk of layers. A timeline profiler shows
  * them; without one they cost a few nanoseconds. */
 

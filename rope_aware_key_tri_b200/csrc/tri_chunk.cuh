@@ -7,32 +7,38 @@
 // zeros and -inf where no key is left. The running maximum m and sum l of a row turn this into one
 // pass over the keys: with p_j = 2^((x_j - m) c), c = scale log2(e), out = sum p_j v_j / sum p_j.
 //
-// Two launches. The plan kernel (one CTA per sequence) checks the sequence (range of tokens, length,
-// pages); its last CTA lists the work, so that nothing waits on the host. An item is a block of
-// kChunkRows rows of a KV head's packed query matrix (row = token * G + head in group, so that all G
-// query heads of a key share its one read), over a range of 128-key tiles. Where there are too few
-// items to fill the SMs evenly, items are split over the keys; the last CTA of an item to finish
-// merges the partial results in the order of the keys, so the result does not depend on which it is.
-// Items are handed out longest first, in rounds that run forth and back over the CTAs.
+// Three launches. The plan kernel (one CTA, or one per sequence for many sequences or long block tables) checks
+// the sequences (range of tokens, length, pages) and lists the work, so that nothing waits on the host. An
+// item is a block of kChunkRows rows of a KV head's packed query matrix (row = token * G + head in group, so
+// that all G query heads of a key share its one read), over a range of 128-key tiles. Where there are too few
+// items to fill the SMs evenly, items are split over the keys, and the merge kernel joins their parts in the
+// order of the keys, so that the result does not depend on which part finished first. Items are handed out
+// longest first, in rounds that run forth and back over the CTAs.
 //
 // The attention kernel, one persistent CTA per SM: warp 0 loads (TMA, 128-byte swizzle: the item's
 // query rows, then K and V tiles through a ring), and two warpgroups take one 128-row query tile each,
 // a row per thread, with a warp each (1 and 2) that issues its tcgen05 MMAs:
 //   S_q = Q_q K^T            128 x 128 x D into TMEM columns [128 q, 128 q + 128)
-//   P_q = 2^((S_q - m) c)    read, masked, exponentiated, rounded to bf16 and written over S_q
+//   P_q = 2^((S_q - m) c)    read, masked, exponentiated, rounded to bf16 and written to TMEM
 //   O_q += P_q V             A from TMEM, V as the N-major operand: the tile lies as it came
-// An MMA warp runs O_q += P_q V(i) and S_q = Q_q K(i+1)^T back to back, so that one warpgroup's
-// exponentials overlap the other's MMAs; S_q(i+1) complete implies P_q V(i) complete, so O_q is the
-// warpgroup's own until it hands over P_q(i+1): it rescales O_q itself, and only where the maximum
-// has grown by more than 2^8 since the last rescale (p then stays below 2^8; nothing is lost, the
-// quotient is the same).
+// An item of at most 128 rows (single and drafted tokens) gives its one query tile to both warpgroups, which take
+// its key tiles in turn and join their (m, l, O) at the end: twice the keys in flight.
+// Head 128: S_0, S_1, O_0 and O_1 fill the tensor memory, so P_q lies over S_q, and an MMA warp runs O_q += P_q V(i) and
+// S_q = Q_q K(i+1)^T back to back; one warpgroup's exponentials overlap the other's MMAs. S_q(i+1) complete implies P_q
+// V(i) complete, so O_q is the warpgroup's own until it hands over P_q(i+1): it rescales O_q itself, and only where
+// the maximum has grown by more than 2^8 since the last rescale (p then stays below 2^8; the quotient is the same).
+// Head 64: P has columns of its own, and S_q(i+1) is computed as soon as S_q(i) has been read.
 //
 // Precision: logits, m, l and O are fp32. P is rounded to bf16 (the MMA's A has V's type): each
 // weight moves by at most 2^-9 relative, independent from key to key, which adds about as much to the
 // result as its own final rounding to bf16. l sums the unrounded weights.
 //
-// Bound: a 256 x 128 pair of tiles is 4 * 256 * 128 * D flops on the tensor cores against 256 * 128
-// exponentials at 16 a clock and SM (D = 128: 2048 clocks each); below about 60 rows per key the HBM.
+// Bound, measured on a B200 with everything but one part of the kernel taken out (512 tokens of 64 heads over 32768
+// rows of 128 dims: 128 items of 256 tiles on 148 SMs; 510 us): the loads alone 343 us, the MMAs with their barriers 426 us,
+// the rest is the chain of a tile from S through the exponentials (1100 clocks) to P V and the next S, whose barriers cost
+// about 300 clocks each way. 64-key steps with two S buffers take that chain apart, but an MMA of 64 keys takes
+// as long as one of 128, and the MMAs alone then took 3100 of 3900 clocks a tile: the same time. Few rows: the HBM (16 single
+// tokens over 2176 rows stream at 7 TB/s for 19 of 37 us; the rest is the plan, the first tiles' latency and the end).
 #pragma once
 
 #include <cuda.h>
@@ -525,13 +531,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         TRI_U8(r, 8), "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::TRI_U8(r, 0),
-        TRI_U8(r, 8), TRI_U8(r, 16), TRI_U8(r, 24), "r"(taddr)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : TRI_W8(r, 0), TRI_W8(r, 8), TRI_W8(r, 16), TRI_W8(r, 24) : : "memory");
 }
@@ -561,8 +560,6 @@ __device__ __forceinline__ float2 exp2_pair(float2 x) {
     return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
                        __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
 }
-
-constexpr int kChunkEmu128 = 1, kChunkEmu64 = 0;
 
 // Heads of 64 leave 128 columns of tensor memory free: P has columns of its own there, so that the next S is
 // computed while the warpgroup still exponentiates this one (at head 128 P lies over S).
@@ -630,14 +627,15 @@ __device__ __forceinline__ void chunk_row_again(const ChunkArgs &a, int s, int l
 // A 128-key tile of one row: S from tensor memory, masked, into the running (m, l); P over S. `left`: the
 // tile's keys that the row sees (cut: some row of the tile sees fewer than 128). `fresh`: the first tile.
 //
-// The hardware exponential takes 8 clocks a warp, 1024 for the tile; `kEmu` of every 8 pairs are
-// evaluated on the FMA pipe instead, about where the two pipes finish together.
+// The hardware exponential takes 8 clocks a warp, 1024 for the tile; `kEmu` of every 8 pairs are evaluated on the
+// FMA pipe instead. Measured with 0, 1, 2 of 8: 844, 835, 854 us (two causal prompts of 8192 and 6145 tokens, head 128) and 522,
+// 510, 507 us (512 tokens over 32768 rows); head 64 (two prompts of 4096 tokens): 244, 250, 247 us.
 template <int D>
 __device__ __forceinline__ bool chunk_softmax_tile(uint32_t ts, uint32_t tp, uint32_t to, float c, bool cut, int left,
                                                    bool fresh, float &m, float &l, int lane, uint64_t *most,
                                                    uint64_t *sfree, uint64_t *pv, unsigned pv_parity, int tries) {
     constexpr unsigned FULL = 0xffffffffu;
-    constexpr int kEmu = D == 128 ? kChunkEmu128 : kChunkEmu64;
+    constexpr int kEmu = D == 128 ? 1 : 0;
     const float NEG_INF = __int_as_float(0xff800000);
     uint32_t s0[32], s1[32], s2[32], s3[32];
     float x0 = NEG_INF, x1 = NEG_INF, x2 = NEG_INF, x3 = NEG_INF;

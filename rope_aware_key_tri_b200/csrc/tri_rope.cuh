@@ -17,6 +17,12 @@
 // A thread's unit is 32 bytes of a row: the 8 + 8 dims of 8 bands, or 16 copied dims; a thread
 // loads kRopeBatch units before the sines are ready, so that the loads, the sines and (for an
 // append) the walk from the token to its slot overlap.
+//
+// Measured on a B200: 2 x 10240 tokens of 32 heads of 128 rotated back in 50 us (6.7 TB/s, the rate of a plain copy);
+// 13758 prompt tokens of one layer appended (8 KV heads, their 32 query heads rotated) in 67 us (5.0 TB/s): there a CTA
+// is one token and lives for the chain starts -> page -> store. 128 threads and 3 units in flight: 67 us; 256 threads
+// with 2, 3, 4: 69 to 87, 74, 72; fewer registers for more CTAs an SM (10, 12, 14 instead of 9): 70, 83, 93. The smallest calls (16 tokens
+// rotated, 8 tokens of 36 layers appended): 2 and 6 us on the device.
 #pragma once
 
 #include <cuda_bf16.h>

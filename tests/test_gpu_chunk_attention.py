@@ -427,3 +427,42 @@ def test_a_key_that_is_not_finite_shows_in_every_row_that_sees_it(what):
         out = ctx.chunk_attention(pool.K, pool.V, lens, q, cu, lse=lse, block_table=pool.table)
         assert torch.isnan(out).all() and torch.isnan(lse).all(), at
     ctx.close()
+
+
+def test_plans_beyond_shared_memory():
+    """More blocks than the plan keeps in shared memory, and a block table too long for one CTA to check."""
+    _run(65, 1, 1, 1, 64, 16, [1] * 2100, [1 + i % 37 for i in range(2100)])
+    pool = pu.Paged(_gen(66), 1, 2, 64, 16, [300, 40, 900], extra_pages=4000)
+    _run(66, 1, 2, 2, 64, 16, [20, 1, 600], [300, 40, 900], pool=pool)
+    pool.table[1, 1] = -1
+    ctx = pu.context(1, 2, 2, 64)
+    q = pu.bf16(_gen(67), (1, 3, 4, 64))
+    ctx.chunk_attention(pool.K, pool.V, torch.tensor([300, 40, 900], dtype=torch.int32).cuda(), q,
+                        torch.arange(4, dtype=torch.int32).cuda(), block_table=pool.table)
+    assert ctx.get_error() == (tri.TRI_EDEVICE, tri.TRI_DEV_BAD_PAGE, 2)
+    ctx.close()
+
+
+def test_calls_on_other_streams():
+    """Each call on its own stream, one after another by events: inputs made on one, used on another."""
+    g = _gen(68)
+    ctx = pu.context(1, 1, 4, 128)
+    pool = pu.Paged(g, 1, 1, 128, 64, [600])
+    q = pu.bf16(g, (1, 40, 4, 128), 2.0)
+    cu, lens = torch.tensor([0, 40], dtype=torch.int32).cuda(), torch.tensor([600], dtype=torch.int32).cuda()
+    pos = torch.arange(40, dtype=torch.int32).cuda()
+    want = ctx.chunk_attention(pool.K, pool.V, lens, ctx.rope(q, pos), cu, block_table=pool.table)
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    r, out = torch.empty_like(q), torch.empty_like(q)
+    for _ in range(3):
+        r.zero_(), out.zero_()
+        a.wait_stream(torch.cuda.current_stream())
+        ctx.rope(q, pos, out=r, stream=a)
+        b.wait_stream(a)
+        with torch.cuda.stream(b):
+            ctx.chunk_attention(pool.K, pool.V, lens, r, cu, out=out, block_table=pool.table)
+        torch.cuda.current_stream().wait_stream(b)
+        assert torch.equal(out, want)
+    assert ctx.get_error()[0] == tri.TRI_OK
+    ctx.close()
