@@ -892,7 +892,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         __syncwarp();
     } else if (warp <= 2) {
         // ---------------- MMAs: one warp for each warpgroup's, so that one's bookkeeping and waits run beside
-        // the other's MMAs (a single warp left the tensor core idle for about 900 of 4100 clocks a round)
+        // the other's MMAs (a single warp left the tensor core idle for about 900 of 4100 clocks a tile)
         const int q = warp - 1;
         const uint32_t id_s = mx_idesc(128), id_o = mx_idesc(D) | (1u << 16);  // V is N-major
         const uint32_t q_low = desc_low(smem_u32(smem + Ly.q), 16u), k_low = desc_low(smem_u32(smem + Ly.ring), 16u);
