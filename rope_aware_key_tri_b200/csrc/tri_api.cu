@@ -1121,7 +1121,8 @@ struct DeviceGuard {
     cudaError_t error;
     explicit DeviceGuard(int device) {
         if (cudaGetDevice(&before) != cudaSuccess) before = -1;
-        error = cudaSetDevice(device);
+        error = before == device ? cudaSuccess : cudaSetDevice(device);
+        if (before == device) before = -1;  // nothing to put back
     }
     ~DeviceGuard() {
         if (before >= 0) cudaSetDevice(before);

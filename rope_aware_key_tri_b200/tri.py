@@ -516,10 +516,15 @@ class TriContext:
         return out
 
     def _tokens(self, name, x, L, T, heads, d):
-        shape = x.shape
-        if len(shape) not in (3, 4) or shape[-3:] != (T, heads, d) or (shape[0] if len(shape) == 4 else 1) != L:
-            raise ValueError(f"{name} must be [{L} layers][{T} tokens][{heads}][{d}], got {tuple(shape)}")
-        return make_rows(x, name, self.device)
+        """make_rows of a tensor whose shape the call gives."""
+        shape, stride = x.shape, x.stride()
+        if len(shape) == 3:
+            shape, stride = (1, *shape), (0, *stride)
+        if tuple(shape) != (L, T, heads, d):
+            raise ValueError(f"{name} must be [{L} layers][{T} tokens][{heads}][{d}], got {tuple(x.shape)}")
+        if x.dtype is not torch.bfloat16 or x.get_device() != self.device or stride[3] != 1:
+            return make_rows(x, name, self.device)  # says what is wrong
+        return tri_rows(x.data_ptr(), stride[0] if L > 1 else 0, stride[1] if T > 1 else 0, stride[2] if heads > 1 else 0)
 
     def append_chunk(self, K, V, pos, lens, K_new, V_new, cu_new, pos_new, block_table=None, lens_out="inplace",
                      rotate=True, q=None, q_out=None, n_pages=None, layer_begin=0, stream=None, check=True):
