@@ -542,9 +542,9 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 
 // 2^x of a pair on the FMA pipe: x = n + f with |f| <= 1/2 (round to nearest by adding 1.5 * 2^23, the
 // reduction of Cody and Waite), 2^f by the degree-4 polynomial of least largest relative error on
-// [-1/2, 1/2] (2.6e-6, found by Remez exchange), n added to the exponent. x <= 127. Below -126, at -infinity
-// and for a NaN: about 2^-126, which weighs nothing beside a row's largest weight (2^-8 at least); a row
-// that sees no key, or a NaN, is told by its maximum.
+// [-1/2, 1/2] (2.6e-6, found by Remez exchange), n added to the exponent. x <= 127. What x = -126 gives is taken off
+// again, so that everything from there down to -infinity is exactly 0: a key that is not seen weighs nothing, however
+// large its value (2^-126 times 3e38 would be 3.5). For a NaN: 0; such a row is told by its maximum.
 __device__ __forceinline__ float2 exp2_pair(float2 x) {
     x.x = fmaxf(x.x, -126.f);
     x.y = fmaxf(x.y, -126.f);
@@ -557,8 +557,12 @@ __device__ __forceinline__ float2 exp2_pair(float2 x) {
     p = __ffma2_rn(p, f, make_float2(0.240247443318367f, 0.240247443318367f));
     p = __ffma2_rn(p, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
     p = __ffma2_rn(p, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
-    return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
-                       __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+    p = make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
+                    __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+    // at x = -126 f is 0 and p the last coefficient, its exponent 126 lower (a subnormal, which the sum keeps)
+    constexpr int kLowest = 0x3f7ffff4 - (126 << 23);  // 0x3f7ffff4: 0.9999992847442627f
+    const float low = -__int_as_float(kLowest);
+    return __fadd2_rn(p, make_float2(low, low));
 }
 
 // Heads of 64 leave 128 columns of tensor memory free: P has columns of its own there, so that the next S is
