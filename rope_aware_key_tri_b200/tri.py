@@ -336,12 +336,12 @@ class TriContext:
         self.handle = tri_create(self.device)
         self.shape = None  # (n_layers, n_kv_heads, group, head_dim) of the loaded statistics
 
-    def _heads(self, name, q, n_kv):
-        # the C ABI takes the head counts from the statistics: what the tensors hold must agree
+    # the C ABI takes the head counts and head_dim from the statistics: what the tensors hold must agree (_cache, _heads)
+    def _heads(self, name, q):
         Hq, d = q.shape[-2], q.shape[-1]
-        if self.shape is not None and (Hq, n_kv, d) != (self.shape[1] * self.shape[2], self.shape[1], self.shape[3]):
-            raise ValueError(f"{name} and the cache have {Hq} and {n_kv} heads of {d}, the loaded statistics "
-                             f"{self.shape[1] * self.shape[2]} and {self.shape[1]} of {self.shape[3]}")
+        if self.shape is not None and (Hq, d) != (self.shape[1] * self.shape[2], self.shape[3]):
+            raise ValueError(f"{name} has {Hq} heads of {d}, the loaded statistics {self.shape[1] * self.shape[2]} of "
+                             f"{self.shape[3]}")
         return Hq
 
     def close(self):
@@ -472,6 +472,8 @@ class TriContext:
         if len(shape) != 5 or len(batch) != 1:
             raise ValueError("K and V must be 5-D: [L][batch][Hkv][cap][d] dense or [L][pages][Hkv][page][d] paged, lens 1-D")
         L, units, H, rows, d = shape
+        if self.shape is not None and (H, d) != (self.shape[1], self.shape[3]):
+            raise ValueError(f"the cache has {H} KV heads of {d}, the loaded statistics {self.shape[1]} of {self.shape[3]}")
         B = batch[0]
         if block_table is None:
             if units != B:
@@ -540,7 +542,7 @@ class TriContext:
         qr = qo = None
         if q is not None:
             q_out = q if q_out is None else q_out
-            Hq = self._heads("q", q, H)
+            Hq = self._heads("q", q)
             qr, qo = self._tokens("q", q, L, T, Hq, d), self._tokens("q_out", q_out, L, T, Hq, d)
         st = _lib.tri_append_chunk(self.handle, kv, kn, vn, self._flat("cu_new", cu_new, torch.int32, (B + 1,)),
                                    self._flat("pos_new", pos_new, torch.int32, (T,)), T, bool(rotate), qr, qo,
@@ -559,7 +561,7 @@ class TriContext:
         T = q.shape[-3]
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        Hq = self._heads("q", q, H)
+        Hq = self._heads("q", q)
         qr, ro = self._tokens("q", q, L, T, Hq, d), self._tokens("out", out, L, T, Hq, d)
         if lse is not None and (lse.dtype is not torch.float32 or lse.numel() != L * T * Hq or not lse.is_contiguous()
                                 or lse.get_device() != self.device):

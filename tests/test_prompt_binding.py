@@ -1,0 +1,37 @@
+"""What the torch-facing calls of the prompt side check before the library sees a pointer, without a GPU: tensors on the CPU are taken
+for the context's device, and the library is handed no context, which it refuses (TRI_EINVAL) once every check has passed."""
+import types
+
+import pytest
+import torch
+
+from rope_aware_key_tri_b200 import tri
+
+STREAM = types.SimpleNamespace(cuda_stream=0)
+
+
+def _context(shape):
+    ctx = tri.TriContext.__new__(tri.TriContext)
+    ctx.device, ctx.handle, ctx.shape = -1, None, shape
+    return ctx
+
+
+def _append(ctx, L=1, H=2, d=64, page=16, pages=4, B=2, T=6, **kw):
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    ints = lambda *s: torch.zeros(s, dtype=torch.int32)
+    units, table = (pages, ints(B, 2)) if page else (B, None)
+    a = dict(block_table=table, stream=STREAM, check=False)
+    a.update(kw)
+    return ctx.append_chunk(bf(L, units, H, page or 32, d), bf(L, units, H, page or 32, d), ints(L, units, H, page or 32), ints(B),
+                            bf(L, T, H, d), bf(L, T, H, d), ints(B + 1), ints(T), **a)
+
+
+@pytest.mark.parametrize("page", [0, 16])
+def test_append_refuses_a_cache_of_other_heads(page):
+    """The library takes heads and head_dim from the statistics: a cache that holds fewer would be written past its end."""
+    assert _append(_context((1, 2, 4, 64)), page=page) == tri.TRI_EINVAL  # (no context)
+    for shape in ((1, 8, 4, 128), (1, 8, 4, 64), (1, 2, 4, 128), (1, 1, 4, 64)):
+        with pytest.raises(ValueError, match="statistics"):
+            _append(_context(shape), page=page)
+        with pytest.raises(ValueError, match="statistics"):
+            _append(_context(shape), page=page, rotate=False)
