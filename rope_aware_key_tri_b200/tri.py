@@ -482,8 +482,9 @@ class TriContext:
         else:
             if block_table.dim() != 2 or block_table.shape[0] != B:
                 raise ValueError(f"block_table must be [batch={B}][max_pages]")
-            if n_pages is not None and n_pages > units:
-                raise ValueError(f"n_pages is {n_pages}, the pools hold {units}")
+            # (the C ABI steps from layer to layer by n_pages)
+            if n_pages is not None and (n_pages > units or L > 1 and n_pages != units):
+                raise ValueError(f"n_pages is {n_pages}, the pools of {L} layers hold {units}")
             table, cap, page, max_pages = self._flat("block_table", block_table, torch.int32), 0, rows, block_table.shape[1]
             n_pages = units if n_pages is None else n_pages
         kv = tri_kv(self._flat("K", K, torch.bfloat16), self._flat("V", V, torch.bfloat16, shape),

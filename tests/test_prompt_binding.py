@@ -35,3 +35,13 @@ def test_append_refuses_a_cache_of_other_heads(page):
             _append(_context(shape), page=page)
         with pytest.raises(ValueError, match="statistics"):
             _append(_context(shape), page=page, rotate=False)
+
+
+def test_fewer_pages_than_the_pools_hold():
+    """n_pages is the pools' layer stride: a part of the pools can be named in a cache of one layer only."""
+    ctx = _context((2, 2, 4, 64))
+    assert _append(ctx, L=1, n_pages=3) == tri.TRI_EINVAL  # (no context)
+    assert _append(ctx, L=2, n_pages=4) == tri.TRI_EINVAL
+    for L, n in ((2, 3), (1, 5), (2, 5)):
+        with pytest.raises(ValueError, match="n_pages"):
+            _append(ctx, L=L, n_pages=n)
