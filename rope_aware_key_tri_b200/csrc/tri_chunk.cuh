@@ -586,46 +586,114 @@ __host__ __device__ inline ChunkSmem chunk_smem(int D) {
     return L;
 }
 
-// The rows whose values are not finite for a reason that may lie in keys they do not see (the MMA
-// multiplies a masked value by a zero weight, and 0 * inf is not 0): row by row, a warp per row, only
-// the keys [k0, k1) that the row sees. Never taken for finite values. Lane's dims: [lane * D / 32, + D / 32).
+// E consecutive bf16 elements, a lane's share of a row.
+template <int E>
+struct ChunkLane {
+    using Vec = unsigned;
+    using Acc = float2;
+};
+template <>
+struct ChunkLane<4> {
+    using Vec = uint2;
+    using Acc = float4;
+};
+template <int E>
+__device__ __forceinline__ void chunk_lane(const typename ChunkLane<E>::Vec &w, float (&x)[E]) {
+    const unsigned *u = reinterpret_cast<const unsigned *>(&w);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+        x[e] = bf16lo(u[e / 2]);
+        x[e + 1] = bf16hi(u[e / 2]);
+    }
+}
+// An MMA multiplies what a row does not see by a zero weight, which leaves nothing of a finite value but makes a NaN of
+// an infinity or a NaN among the values. So a dim of a row that came out not finite, where the item goes on past the
+// keys that the row sees and one of those hidden values is not finite in that dim, is computed again over the seen
+// keys of the item alone: by a warp, on the CUDA cores (weights in fp32, about 0.2 us a key), until every dim in question has
+// met a NaN. What is not finite for a reason that the row does see stays as it is; telling so costs a look at the item's
+// hidden values (at most 383 keys). `in_block`: the row among the block's, `slot` where the item's part lies.
+// Its code is kept small, for calls that never run it pay for its size: 1 us here (of the 40 for 16 single tokens), 5 us
+// when the merge kernel held it.
 template <int D>
-__device__ __forceinline__ void chunk_row_again(const ChunkArgs &a, int s, int lr, int g, const uint16_t *q, int k0, int k1,
-                                             float (&acc)[D / 32], float &m, float &l) {
-    constexpr int E = D / 32;
+__device__ __forceinline__ void chunk_row_again(const ChunkArgs &a, const ChunkEntry &en, int lr, int g, long long slot, int in_block) {
+    constexpr int E = D / 32;  // lane's dims: [lane * E, + E)
     constexpr unsigned FULL = 0xffffffffu;
-    const int lane = threadIdx.x & 31;
     const float NEG_INF = __int_as_float(0xff800000);
-    float qv[E];
+    using Vec = typename ChunkLane<E>::Vec;
+    const int lane = threadIdx.x & 31, shift = __ffs(a.group) - 1;
+    const int tok = en.tok0 + (in_block >> shift), head = g * a.group + (in_block & (a.group - 1));
+    const int k0 = en.kt0 * 128, end = min(en.len, en.kt1 * 128);
+    const int seen = max(k0, min(end, en.first + (in_block >> shift))), hide = end - seen;
+    const bool part = en.nsplit > 1;
+    if (hide <= 0) return;
+    using Acc = typename ChunkLane<E>::Acc;
+    Vec *out = reinterpret_cast<Vec *>(a.out + lr * a.o_l + tok * a.o_t + head * a.o_h + lane * E);
+    Acc *acc_out = reinterpret_cast<Acc *>(a.part + ((slot * (D / 4) + lane * E / 4) * 128 + (in_block & 127)) * 4 + lane * E % 4);
+    unsigned todo = 0, hidden = 0;  // this lane's dims that are not finite here, and in a hidden value
+    float was[E], qv[E], acc[E], m = NEG_INF, l = 0.f;
+    if (part) *reinterpret_cast<Acc *>(was) = *acc_out; else chunk_lane<E>(*out, was);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        qv[e] = __uint_as_float((unsigned)q[lane * E + e] << 16);
+        if (!(fabsf(was[e]) < __int_as_float(0x7f800000))) todo |= 1u << e;
         acc[e] = 0.f;
     }
-    m = NEG_INF;
-    l = 0.f;
-    for (int j = k0; j < k1; ++j) {
-        long long row;
+    if (!__any_sync(FULL, todo != 0)) return;
+    chunk_lane<E>(*reinterpret_cast<const Vec *>(a.q + lr * a.q_l + tok * a.q_t + head * a.q_h + lane * E), qv);
+#pragma unroll 1
+    for (int i = 0; i < end - k0; ++i) {
+        const int j = i < hide ? seen + i : k0 + i - hide;  // the hidden keys, then those that it sees
+        int unit = lr * a.batch + en.s, rows = a.cap_u, off = j;
         if (a.paged) {
-            const int pg = __ldg(a.block_table + (long long)s * a.max_pages + j / a.page_size);
-            row = (((long long)lr * a.n_pages + pg) * a.n_kv + g) * (long long)a.page_size + j % a.page_size;
-        } else {
-            row = (((long long)lr * a.batch + s) * a.n_kv + g) * (long long)a.cap_u + j;
+            const int p = j / a.page_size;
+            rows = a.page_size;
+            off = j - p * rows;
+            unit = lr * a.n_pages + __ldg(a.block_table + (long long)en.s * a.max_pages + p);
         }
-        float x = 0.f;
+        const long long at = (((long long)unit * a.n_kv + g) * rows + off) * D + lane * E;
+        float v[E], k[E], x = 0.f;
+        chunk_lane<E>(*reinterpret_cast<const Vec *>(a.V + at), v);
+        chunk_lane<E>(*reinterpret_cast<const Vec *>(a.K + at), k);
+        if (i < hide) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) x += qv[e] * __uint_as_float((unsigned)a.K[row * D + lane * E + e] << 16);
+            for (int e = 0; e < E; ++e)
+                if (!(fabsf(v[e]) < __int_as_float(0x7f800000))) hidden |= 1u << e;
+            if (i == hide - 1) {
+                todo &= hidden;
+                if (!__any_sync(FULL, todo != 0)) return;
+            }
+            continue;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) x += qv[e] * k[e];
+#pragma unroll
         for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
         x *= a.c;
-        const float mn = fmaxf(m, x);
-        const float corr = m == mn ? 1.f : ex2_approx(m - mn);
-        const float p = ex2_approx(x - (mn == NEG_INF ? 0.f : mn));
-        l = l * corr + p;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            acc[e] = acc[e] * corr + p * __uint_as_float((unsigned)a.V[row * D + lane * E + e] << 16);
+        const float mn = fmaxf(m, x), z = mn == NEG_INF ? 0.f : mn;
+        const float corr = ex2_approx(m - z), p = ex2_approx(x - z);
         m = mn;
+        l = l * corr + p;
+        bool open = false;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            acc[e] = acc[e] * corr + p * v[e];
+            open = open || ((todo >> e & 1u) && acc[e] == acc[e]);
+        }
+        if (!__any_sync(FULL, open)) break;
     }
+    // a part goes by the maximum that it was written with; one that sees no key weighs nothing, whatever it holds
+    const float scale = l == 0.f ? 0.f : part ? ex2_approx(m - a.part_ml[(slot * 128 + (in_block & 127)) * 2]) : 1.f / l;
+    unsigned w[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (todo >> e & 1u) was[e] = acc[e] * scale;
+        if (e & 1) w[e / 2] = pack_bf16(was[e - 1], was[e]);
+    }
+    if (part) *acc_out = *reinterpret_cast<Acc *>(was); else *out = *reinterpret_cast<Vec *>(w);
+}
+// A CTA's item of round r: forth in even rounds, back in odd ones.
+__device__ __forceinline__ unsigned chunk_item(int r) {
+    const int pos = (r & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
+    return (unsigned)r * gridDim.x + (unsigned)pos;
 }
 
 // A 128-key tile of one row: S from tensor memory, masked, into the running (m, l); P over S. `left`: the
@@ -806,11 +874,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
     const int G = a.group, LH = a.n_layers * a.n_kv;
     const unsigned n_items = (unsigned)a.head->n_entries * (unsigned)LH;  // below 2^31
-    // this CTA's item of round r: forth in even rounds, back in odd ones
-    auto item_of = [&](int r) {
-        const int pos = (r & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
-        return (unsigned)r * gridDim.x + (unsigned)pos;
-    };
     auto fail = [&](const ChunkEntry &e, int lh) {
         record_status(a.status, kDevTimeout, ((long long)(lh / a.n_kv) * a.batch + e.s) * a.n_kv + lh % a.n_kv);
         *abort_flag = 1;
@@ -824,7 +887,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         int k = 0, nq = 0;      // ring fills so far, query tiles loaded so far
         bool ok = true;
         for (int r = 0; ok && !*abort_flag; ++r) {
-            const unsigned it = item_of(r);
+            const unsigned it = chunk_item(r);
             if (it >= n_items) break;
             const ChunkEntry e = a.entries[it / LH];
             const int lh = (int)(it % LH), lr = lh / a.n_kv, g = lh % a.n_kv;
@@ -919,7 +982,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             at.step();
         };
         for (int r = 0; ok && !*abort_flag; ++r) {
-            const unsigned it = item_of(r);
+            const unsigned it = chunk_item(r);
             if (it >= n_items) break;
             const ChunkEntry e = a.entries[it / LH];
             // (values that the compiler shall know to be the same in every lane go through a shuffle)
@@ -1043,10 +1106,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t ts = tmem + lanes + 128u * q, to = tmem + lanes + 256u + (uint32_t)(D * q);
         const uint32_t tp = chunk_apart(D) ? tmem + lanes + 384u + 64u * q : ts;
         unsigned ns = 0, no = 0, nx = 0;  // S tiles, items, paired items so far
-        bool ok = true;
+        bool ok = true, again = false;    // again: a row of this thread may need chunk_row_again
         for (int r = 0; ok && !*abort_flag; ++r) {
-            const unsigned it = item_of(r);
-            if (it >= n_items) break;
+            const unsigned it = chunk_item(r);
+            if (it >= n_items) {
+                // what hidden values spoilt is mended last, when no role waits for this warp any more: it may take far
+                // longer than their bounded waits
+                if (__any_sync(FULL, again)) {
+                    __syncwarp();  // the rows that other lanes wrote
+#pragma unroll 1
+                    for (int x = 0; x < r; ++x) {
+                        const unsigned xt = chunk_item(x);
+                        const ChunkEntry &e = a.entries[xt / LH];
+                        if (e.pair && q == 1) continue;
+                        const int lh = (int)(xt % LH), lr = lh / a.n_kv, tile = e.pair ? 0 : q;
+                        const long long slot = ((long long)e.slot * LH + (long long)lh * e.nsplit + e.split) * 2 + tile;
+                        const int row0 = 128 * tile + (warp & 3) * 32;
+#pragma unroll 1
+                        for (int row = row0; row < min(e.ntok * G, row0 + 32); ++row)
+                            chunk_row_again<D>(a, e, lr, lh - lr * a.n_kv, slot, row);
+                    }
+                }
+                break;
+            }
             const ChunkEntry *ep = a.entries + it / LH;
             const int lh = (int)(it % LH);
             float m = NEG_INF, l = 0.f;
@@ -1099,7 +1181,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // ---- the result of the item, or its part ----
             const int4 *e4 = reinterpret_cast<const int4 *>(ep);
             const int4 ea = __ldcg(e4), eb = __ldcg(e4 + 1), ec = __ldcg(e4 + 2);
-            const int len = ea.w, kt0 = eb.y, kt1 = eb.z, nsplit = ec.x;
+            const int len = ea.w, kt1 = eb.z, nsplit = ec.x;
             float w0 = 1.f, w1 = 0.f;
             if (m == NEG_INF) l = 0.f;                        // no key: what is left of its zero weights goes
             m *= a.c;                                         // the log2 domain (-inf stays)
@@ -1197,32 +1279,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     a.lse[((long long)lr * a.n_tokens + trow) * (a.n_kv * G) + head] =
                         l == 0.f ? NEG_INF : (m + log2f(l)) * 0.6931471805599453f;
             }
-            unsigned again = __ballot_sync(FULL, mine && odd && limit < min(len, kt1 * 128));
-            __syncwarp();
-            while (again) {  // see chunk_row_again
-                const int src = __ffs(again) - 1;
-                again &= again - 1;
-                const int rt = __shfl_sync(FULL, tok, src), rh = __shfl_sync(FULL, hd, src), rl = __shfl_sync(FULL, limit, src);
-                float acc[D / 32], rm, rs;
-                chunk_row_again<D>(a, ea.x, lr, g, a.q + lr * a.q_l + (ea.y + rt) * a.q_t + (g * G + rh) * a.q_h,
-                                   kt0 * 128, min(rl, kt1 * 128), acc, rm, rs);
-                const int rr = (warp & 3) * 32 + src;
-                if (nsplit == 1) {
-                    uint16_t *dst = a.out + lr * a.o_l + (ea.y + rt) * a.o_t + (g * G + rh) * a.o_h;
-                    const float ri = rs == 0.f ? 0.f : 1.f / rs;
-#pragma unroll
-                    for (int x = 0; x < D / 32; ++x)
-                        dst[lane * (D / 32) + x] = (uint16_t)(pack_bf16(rs == 0.f ? 0.f : acc[x] * ri, 0.f) & 0xffffu);
-                } else {
-#pragma unroll
-                    for (int x = 0; x < D / 32; ++x) {
-                        const int dim = lane * (D / 32) + x;
-                        a.part[((slot * (D / 4) + dim / 4) * 128 + rr) * 4 + dim % 4] = acc[x];
-                    }
-                    if (lane == 0) *reinterpret_cast<float2 *>(a.part_ml + (slot * 128 + rr) * 2) = make_float2(rm, rs);
-                }
-                __syncwarp();
-            }
+            again |= mine && odd && limit < min(len, kt1 * 128);
         }
     }
     tc_fence_before();
