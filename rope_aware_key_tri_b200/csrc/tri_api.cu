@@ -71,6 +71,8 @@ struct tri_ctx {
         size_t bytes = 0;
     } ws_new_len, ws_plan, ws_part;
     std::vector<void *> ws_old;
+    // CTAs done of tri_append_chunk and of the attention's plan, zero between calls. Not part of the blocks above, which a
+    // call may replace and then fail.
     unsigned *d_ticket = nullptr;
     bool chunk_ready[2] = {false, false};  // the attention kernels' shared memory has been opted in to
     // device bookkeeping
@@ -1459,11 +1461,11 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
                  o_merges = take(sizeof(tri::ChunkEntry) * (size_t)a.max_slots),
                  o_entries = take(sizeof(tri::ChunkEntry) * (size_t)entries);
     const size_t part_floats = (size_t)a.max_slots * 2 * 128 * D, ml_floats = (size_t)a.max_slots * 2 * 128 * 2;
-    const bool fresh = off > c->ws_plan.bytes;
     if ((st = ensure_block(c, &c->ws_plan, off, "cudaMalloc(attention plan)")) != TRI_OK) return st;
     if ((st = ensure_block(c, &c->ws_part, (part_floats + ml_floats) * sizeof(float), "cudaMalloc(attention parts)")) != TRI_OK)
         return st;
     unsigned char *ws = static_cast<unsigned char *>(c->ws_plan.p);
+    a.ticket = c->d_ticket + 1;
     a.head = reinterpret_cast<tri::ChunkHead *>(ws + o_head);
     a.seqs = reinterpret_cast<tri::ChunkSeq *>(ws + o_seqs);
     a.base = reinterpret_cast<int *>(ws + o_base);
@@ -1473,10 +1475,6 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
     a.part = static_cast<float *>(c->ws_part.p);
     a.part_ml = a.part + part_floats;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (fresh) {
-        ce = cudaMemsetAsync(a.head, 0, sizeof(tri::ChunkHead), cs);  // the ticket; every plan leaves it at zero
-        if (ce != cudaSuccess) return cuda_fail(c, ce, "cudaMemsetAsync(plan)");
-    }
 
     CUtensorMap qmap, kmap, vmap;
     const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)n_tokens, (cuuint64_t)L};
@@ -1571,7 +1569,7 @@ tri_status tri_create(tri_ctx **out, int device) {
     if (cudaMalloc(&c->d_status, sizeof(unsigned long long)) != cudaSuccess ||
         cudaMalloc(&c->d_counter, 2 * sizeof(unsigned int)) != cudaSuccess ||
         cudaMalloc(&c->d_turns, sizeof(double) * kMaxRopeDim / 2) != cudaSuccess ||
-        cudaMalloc(&c->d_ticket, sizeof(unsigned)) != cudaSuccess ||
+        cudaMalloc(&c->d_ticket, 2 * sizeof(unsigned)) != cudaSuccess ||
         cudaMalloc(&c->d_fail_count, sizeof(unsigned)) != cudaSuccess ||
         cudaMalloc(&c->d_fail_units, sizeof(int32_t) * kFailCap) != cudaSuccess) {
         tri_destroy(c);
@@ -1579,7 +1577,7 @@ tri_status tri_create(tri_ctx **out, int device) {
     }
     if (cudaMemset(c->d_status, 0, sizeof(unsigned long long)) != cudaSuccess ||
         cudaMemset(c->d_counter, 0, 2 * sizeof(unsigned int)) != cudaSuccess ||
-        cudaMemset(c->d_ticket, 0, sizeof(unsigned)) != cudaSuccess ||
+        cudaMemset(c->d_ticket, 0, 2 * sizeof(unsigned)) != cudaSuccess ||
         cudaMemset(c->d_fail_count, 0, sizeof(unsigned)) != cudaSuccess) {
         tri_destroy(c);
         return TRI_ECUDA;

@@ -78,7 +78,6 @@ struct __align__(16) ChunkSeq {
 struct ChunkHead {
     int n_entries;            // lines of the plan
     int n_groups;             // blocks that are split
-    unsigned ticket;          // plan CTAs done (back to 0 at the end)
 };
 
 struct ChunkArgs {
@@ -98,6 +97,7 @@ struct ChunkArgs {
     long long o_l, o_t, o_h;
     float *lse;               // [n_layers][n_tokens][Hq] or null
     const uint16_t *K, *V;
+    unsigned *ticket;         // plan CTAs done (the context's; back to 0 at the end)
     // workspace
     ChunkHead *head;
     ChunkSeq *seqs;           // [batch]
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
             a.seqs[s0] = ChunkSeq{lo, hi - lo, len, bad};
             if (bad) record_status(a.status, bad, (long long)s0 * a.n_kv);
             __threadfence();
-            sh_last = atomicAdd(&a.head->ticket, 1u) == gridDim.x - 1;
+            sh_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
         }
     }
     if (!alone) {
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
         sh_run = 0;
         sh_sum = 0;
         sh_max = 0;
-        if (!alone) a.head->ticket = 0;
+        if (!alone) *a.ticket = 0;
     }
     __syncthreads();
     const int G = a.group, tpb = kChunkRows / G;
