@@ -394,7 +394,8 @@ TRI_API tri_status tri_append_chunk(tri_ctx *ctx, const tri_kv *kv, const tri_ro
  *   q       tri_rows [n_layers][n_tokens][n_kv_heads * group]: post-RoPE queries of the new tokens of all
  *           sequences (strides above 0 in each dimension of more than one element)
  *   cu_q    int32 [batch + 1] device: sequence s has the query tokens [cu_q[s], cu_q[s + 1]), its last n
- *   scale   > 0: logits are scale q . k (1 / sqrt(head_dim) for the attention of tri_decode_attention)
+ *   scale   > 0: logits are scale q . k (1 / sqrt(head_dim) for the attention of tri_decode_attention); scale log2(e) must be
+ *           a normal fp32 number (2^-126 and above, finite)
  *   causal  0: every query sees all lens[s] rows. Otherwise query i of n sees the rows [0, lens[s] - n + i + 1):
  *           rows are ordered by slot, so after a prune too it sees all that is kept of what came before it
  *   out     tri_rows like q, written: bf16

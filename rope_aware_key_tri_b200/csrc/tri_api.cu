@@ -17,6 +17,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <limits>
 #include <mutex>
 #include <vector>
 
@@ -1373,7 +1374,9 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
     if (!c || !kv || !cu_q) return TRI_EINVAL;
     c->last_error[0] = 0;
     if (!c->loaded) return TRI_ESTATE;
-    if (n_tokens < 0 || !(scale > 0.0) || !std::isfinite(scale)) return TRI_EINVAL;
+    // the kernel's factor, to the base of its exponentials: in fp32 neither zero nor subnormal nor infinite
+    const float c_log2 = (float)(scale * 1.4426950408889634);
+    if (n_tokens < 0 || !(c_log2 >= std::numeric_limits<float>::min()) || !std::isfinite(c_log2)) return TRI_EINVAL;
     long long cap_u = 0;
     tri_status st = check_cache(c, kv, false, &cap_u);
     if (st != TRI_OK) return st;
@@ -1426,7 +1429,7 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
     // the largest box that no page boundary cuts
     a.piece_rows = !paged || kv->page_size % 128 == 0 ? 128 : kv->page_size % 64 == 0 ? 64 : kv->page_size % 32 == 0 ? 32 : 16;
     a.sm_count = c->sm_count;
-    a.c = (float)(scale * 1.4426950408889634);
+    a.c = c_log2;
     a.q = static_cast<const uint16_t *>(q->data);
     a.q_l = q->layer_stride;
     a.q_t = q->token_stride;

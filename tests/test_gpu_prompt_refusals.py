@@ -1,0 +1,66 @@
+"""Calls of the prompt side that are refused on the host: the outputs stay as they were."""
+import math
+
+import pytest
+import torch
+
+import prompt_util as pu
+from rope_aware_key_tri_b200 import tri
+
+pytestmark = pytest.mark.gpu
+
+
+class Case:
+    """One attention and one append call of 8 tokens of two sequences, made with what is changed."""
+
+    def __init__(self, L=1):
+        g = torch.Generator().manual_seed(100)
+        self.ctx = pu.context(2, 2, 2, 64)
+        self.pool = pu.Paged(g, L, 2, 64, 16, [40, 40])
+        self.q = pu.bf16(g, (L, 8, 4, 64))
+        self.cu = torch.tensor([0, 4, 8], dtype=torch.int32).cuda()
+        self.lens = torch.tensor([20, 30], dtype=torch.int32).cuda()
+        self.pos = torch.arange(8, dtype=torch.int32).cuda()
+        self.out = torch.full((L, 8, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        self.before = [x.clone() for x in self._all()]
+
+    def _all(self):
+        p = self.pool
+        return p.K, p.V, p.P, self.q, self.lens, self.out
+
+    def attend(self, **kw):
+        a = dict(q=self.q, cu_q=self.cu, out=self.out, block_table=self.pool.table, check=False)
+        a.update(kw)
+        return self.ctx.chunk_attention(self.pool.K, self.pool.V, self.lens, **a)
+
+    def append(self, **kw):
+        a = dict(K_new=self.q[:, :, :2], V_new=self.q[:, :, 2:], cu_new=self.cu, pos_new=self.pos, block_table=self.pool.table,
+                 check=False)
+        a.update(kw)
+        return self.ctx.append_chunk(self.pool.K, self.pool.V, self.pool.P, self.lens, **a)
+
+    def unchanged(self):
+        torch.cuda.synchronize()
+        assert self.ctx.get_error()[0] == tri.TRI_OK
+        assert all(torch.equal(a, b) for a, b in zip(self.before, self._all()))
+        self.ctx.close()
+
+
+def test_scales_that_fp32_does_not_hold():
+    c = Case()
+    for scale in (1e-300, 1e-46, 2.0 ** -128, 1e39, 1e300, 5e-324):
+        assert c.attend(scale=scale) == tri.TRI_EINVAL, scale
+    c.unchanged()
+
+
+def test_the_smallest_scale():
+    """All weights equal: the mean of the values that each query sees (bf16: half a step of the result, and fp32 sums)."""
+    c = Case()
+    assert c.attend(scale=2.0 ** -126) == tri.TRI_OK
+    for b, m in enumerate((20, 30)):
+        v = c.pool.rows(c.pool.V, b, m)[0].double()
+        for i in range(4):
+            want = v[:, :m - 3 + i].mean(1)
+            got = c.out[0, 4 * b + i].double().view(2, 2, 64)
+            assert ((got - want[:, None]).abs() <= 2.0 ** -8 * want.abs()[:, None] + 2.0 ** -18 * v.abs().max()).all()
+    c.ctx.close()
