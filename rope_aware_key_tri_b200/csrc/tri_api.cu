@@ -406,7 +406,7 @@ tri_status check_call(tri_ctx *c, const tri_kv *kv, const int32_t *t, int32_t bu
                       int mode, long long *cap_out) {
     if (!c || !kv || !t) return TRI_EINVAL;
     if (!c->loaded) return TRI_ESTATE;
-    if (kv->batch < 1 || kv->n_layers < 1 || kv->layer_begin < 0 || kv->layer_begin + kv->n_layers > c->L)
+    if (kv->batch < 1 || kv->n_layers < 1 || kv->layer_begin < 0 || kv->layer_begin > c->L - kv->n_layers)
         return TRI_EINVAL;
     const bool paged = kv->block_table != nullptr;
     long long cap_u;
@@ -855,7 +855,7 @@ tri_status run_noalloc(tri_ctx *c, const tri_kv *kv, const int32_t *t, int32_t b
                       "tri_prune_noalloc: the max-over-offsets mode needs scratch that only tri_prune allocates");
         return TRI_EUNSUPPORTED;
     }
-    if (kv->batch < 1 || kv->n_layers < 1 || kv->layer_begin < 0 || kv->layer_begin + kv->n_layers > c->L)
+    if (kv->batch < 1 || kv->n_layers < 1 || kv->layer_begin < 0 || kv->layer_begin > c->L - kv->n_layers)
         return TRI_EINVAL;
     const bool paged = kv->block_table != nullptr;
     long long cap_u;
@@ -988,7 +988,7 @@ bool pick_attend(int D, int G, AttFn *main_fn, AttFn *combine_fn) {
 tri_status run_attend(tri_ctx *c, const tri_kv *kv, const void *q, float *out, void *stream) {
     if (!c || !kv || !q || !out) return TRI_EINVAL;
     if (!c->loaded) return TRI_ESTATE;
-    if (kv->batch < 1 || kv->n_layers < 1 || kv->layer_begin < 0 || kv->layer_begin + kv->n_layers > c->L)
+    if (kv->batch < 1 || kv->n_layers < 1 || kv->layer_begin < 0 || kv->layer_begin > c->L - kv->n_layers)
         return TRI_EINVAL;
     const bool paged = kv->block_table != nullptr;
     long long cap_u;
@@ -1273,7 +1273,7 @@ tri_status run_rope(tri_ctx *c, const tri_rows *x, const tri_rows *out, int n_la
 
 // The cache of a call that brings new tokens: shape, alignment, device memory; *cap_out the unit capacity.
 tri_status check_cache(tri_ctx *c, const tri_kv *kv, bool append, long long *cap_out) {
-    if (kv->batch < 1 || kv->n_layers < 1 || kv->layer_begin < 0 || kv->layer_begin + kv->n_layers > c->L)
+    if (kv->batch < 1 || kv->n_layers < 1 || kv->layer_begin < 0 || kv->layer_begin > c->L - kv->n_layers)
         return TRI_EINVAL;
     const bool paged = kv->block_table != nullptr;
     if (paged) {
@@ -1827,7 +1827,7 @@ tri_status append_impl(tri_ctx *c, const tri_kv *kv, const void *K_new, const vo
     if (!c->loaded) return TRI_ESTATE;
     if (c->D != 64 && c->D != 128) return TRI_EUNSUPPORTED;
     if (!kv->block_table || !kv->K || !kv->V || !kv->pos || !kv->lens || !kv->lens_out) return TRI_EINVAL;
-    if (kv->batch < 1 || kv->n_layers < 1 || kv->layer_begin < 0 || kv->layer_begin + kv->n_layers > c->L)
+    if (kv->batch < 1 || kv->n_layers < 1 || kv->layer_begin < 0 || kv->layer_begin > c->L - kv->n_layers)
         return TRI_EINVAL;
     if (kv->page_size < 16 || kv->page_size % 16 != 0 || kv->max_pages < 1 || kv->n_pages < 1) return TRI_EINVAL;
     const void *dev[] = {kv->K, kv->V, kv->pos, kv->lens, kv->lens_out, kv->block_table, K_new, V_new, pos_new};

@@ -64,3 +64,21 @@ def test_the_smallest_scale():
             got = c.out[0, 4 * b + i].double().view(2, 2, 64)
             assert ((got - want[:, None]).abs() <= 2.0 ** -8 * want.abs()[:, None] + 2.0 ** -18 * v.abs().max()).all()
     c.ctx.close()
+
+
+def test_layers_past_the_statistics():
+    """Also where the sum of the first layer and their number does not fit an int."""
+    c = Case()
+    p = c.pool
+    for first in (2, 3, 2**31 - 1):
+        assert c.attend(layer_begin=first) == tri.TRI_EINVAL
+        assert c.append(layer_begin=first) == tri.TRI_EINVAL
+        t = torch.full((2,), 99, dtype=torch.int32, device="cuda")
+        kw = dict(block_table=p.table, layer_begin=first, check=False)
+        assert c.ctx.prune(p.K, p.V, p.P, c.lens, t, 8, **kw) == tri.TRI_EINVAL
+        assert c.ctx.prune_noalloc(p.K, p.V, p.P, c.lens, t, 8, **kw) == tri.TRI_EINVAL
+        assert c.ctx.score(p.K, c.lens, t, **kw) == tri.TRI_EINVAL
+        assert c.ctx.decode_attention(p.K, p.V, c.lens, c.q[:, :2].contiguous(), **kw) == tri.TRI_EINVAL
+        assert c.ctx.append(p.K, p.V, p.P, c.lens, p.table, c.q[:, :2, :2].contiguous(), c.q[:, :2, 2:].contiguous(),
+                            c.pos[:2].contiguous(), layer_begin=first, check=False) == tri.TRI_EINVAL
+    c.unchanged()
