@@ -398,7 +398,7 @@ TRI_API tri_status tri_append_chunk(tri_ctx *ctx, const tri_kv *kv, const tri_ro
  *           a normal fp32 number (2^-126 and above, finite)
  *   causal  0: every query sees all lens[s] rows. Otherwise query i of n sees the rows [0, lens[s] - n + i + 1):
  *           rows are ordered by slot, so after a prune too it sees all that is kept of what came before it
- *   out     tri_rows like q, written: bf16
+ *   out     tri_rows like q, written: bf16. It must not overlap q or the cache
  *   lse     fp32 [n_layers][n_tokens][n_kv_heads * group] device, written, or NULL: the natural logarithm of the sum of
  *           exp(logit), with which attentions over other rows can be joined
  * A query that sees no row (lens[s] of 0, or a query in front of the first row) gets zeros and an lse of -infinity. Rows

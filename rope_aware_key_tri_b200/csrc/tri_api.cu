@@ -1184,6 +1184,40 @@ tri_status check_rows(tri_ctx *c, const tri_rows *r, long long layers, long long
     return TRI_OK;
 }
 
+// Whether written rows lie on rows that the call reads: told where both have the same strides (some x_i with |x_i| < n_i bring
+// the bases closer than a row), or start at the same place. Rows interleaved with other strides are the caller's to keep apart.
+bool rows_meet(const tri_rows *r, const tri_rows *w, long long layers, long long tokens, long long heads, int D) {
+    struct Dim {
+        long long n, stride, other;
+    } d[3] = {{layers, r->layer_stride, w->layer_stride}, {tokens, r->token_stride, w->token_stride}, {heads, r->head_stride, w->head_stride}};
+    std::sort(d, d + 3, [](const Dim &x, const Dim &y) { return x.stride > y.stride; });
+    bool same = true;
+    for (const Dim &x : d) same = same && (x.n == 1 || x.stride == x.other);
+    if (!same) return r->data == w->data;
+    long long near[8] = {((long long)reinterpret_cast<uintptr_t>(w->data) - (long long)reinterpret_cast<uintptr_t>(r->data)) / 2};
+    int count = 1;
+    for (const Dim &x : d) {  // each distance left, less the multiples of the stride on either side of it
+        if (x.n == 1 || x.stride == 0) continue;
+        long long next[8];
+        int k = 0;
+        for (int i = 0; i < count; ++i)
+            for (long long t = near[i] / x.stride - (near[i] < 0), end = t + 1; t <= end; ++t)
+                next[k++] = near[i] - std::min(std::max(t, 1 - x.n), x.n - 1) * x.stride;
+        std::copy(next, next + k, near);
+        count = k;
+    }
+    return std::any_of(near, near + count, [&](long long x) { return x > -D && x < D; });
+}
+// One and the same rows.
+bool same_rows(const tri_rows *a, const tri_rows *b, long long layers, long long tokens, long long heads) {
+    return a->data == b->data && (layers == 1 || a->layer_stride == b->layer_stride) &&
+           (tokens == 1 || a->token_stride == b->token_stride) && (heads == 1 || a->head_stride == b->head_stride);
+}
+tri_status overlap_error(tri_ctx *c, const char *what) {
+    std::snprintf(c->last_error, sizeof c->last_error, "%s", what);
+    return TRI_EINVAL;
+}
+
 tri::RowSet row_set(const tri_rows *src, const tri_rows *dst, int heads) {
     tri::RowSet s;
     std::memset(&s, 0, sizeof s);
@@ -1260,6 +1294,8 @@ tri_status run_rope(tri_ctx *c, const tri_rows *x, const tri_rows *out, int n_la
     tri_status st = check_rows(c, x, n_layers, n_tokens, n_heads, head_dim, false, "tri_rope: x");
     if (st == TRI_OK) st = check_rows(c, out, n_layers, n_tokens, n_heads, head_dim, true, "tri_rope: out");
     if (st != TRI_OK) return st;
+    if (!same_rows(x, out, n_layers, n_tokens, n_heads) && rows_meet(x, out, n_layers, n_tokens, n_heads, head_dim))
+        return overlap_error(c, "tri_rope: out overlaps x without being x");
     const DeviceGuard guard(c->device);
     if (guard.error != cudaSuccess) return cuda_fail(c, guard.error, "cudaSetDevice");
     tri::RopeArgs a;
@@ -1323,6 +1359,8 @@ tri_status run_append_chunk(tri_ctx *c, const tri_kv *kv, const tri_rows *K_new,
         if (q) {
             if ((st = check_rows(c, q, L, n_tokens, Hq, D, false, "tri_append_chunk: q")) != TRI_OK) return st;
             if ((st = check_rows(c, q_out, L, n_tokens, Hq, D, true, "tri_append_chunk: q_out")) != TRI_OK) return st;
+            if (!same_rows(q, q_out, L, n_tokens, Hq) && rows_meet(q, q_out, L, n_tokens, Hq, D))
+                return overlap_error(c, "tri_append_chunk: q_out overlaps q without being q");
             a.q = row_set(q, q_out, Hq);
         }
         a.k = row_set(K_new, nullptr, Hkv);
@@ -1385,6 +1423,7 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
     if (n_tokens == 0) return TRI_OK;
     if ((st = check_rows(c, q, L, n_tokens, Hq, D, false, "tri_chunk_attention: q")) != TRI_OK) return st;
     if ((st = check_rows(c, out, L, n_tokens, Hq, D, true, "tri_chunk_attention: out")) != TRI_OK) return st;
+    if (rows_meet(q, out, L, n_tokens, Hq, D)) return overlap_error(c, "tri_chunk_attention: out overlaps q");
     if (lse && (!aligned(lse, 4) || !on_device(c, lse))) return TRI_EINVAL;
     // a dimension of one element has no stride of its own; the others must step over at least a row
     const long long dims[3] = {Hq, n_tokens, L};

@@ -82,3 +82,38 @@ def test_layers_past_the_statistics():
         assert c.ctx.append(p.K, p.V, p.P, c.lens, p.table, c.q[:, :2, :2].contiguous(), c.q[:, :2, 2:].contiguous(),
                             c.pos[:2].contiguous(), layer_begin=first, check=False) == tri.TRI_EINVAL
     c.unchanged()
+
+
+def test_outputs_that_lie_on_their_inputs():
+    """Interleaved with them, or in place where a call allows it, they are taken."""
+    c = Case(L=2)
+    q, hit = c.q, tri.TRI_EINVAL
+    assert c.attend(out=q) == hit
+    wide = torch.zeros((2, 16, 12, 64), dtype=torch.bfloat16, device="cuda")
+    wide[:, :8, :4] = q
+    x = wide[:, :8, :4]
+    for other in (wide[:, :8, 1:5], wide[:, 1:9, :4], wide[:, 7:15, 3:7], wide[:, :8, 3:7]):  # on some of its rows
+        assert c.attend(q=x, out=other) == hit
+        assert c.attend(q=other, out=x) == hit
+        assert c.ctx.rope(x, c.pos, out=other, check=False) == hit
+        assert c.append(q=x, q_out=other) == hit
+    flat = wide.view(-1)
+    shifted = flat[8:8 + q.numel()].view(2, 8, 4, 64)
+    assert c.attend(q=flat[:q.numel()].view(2, 8, 4, 64), out=shifted) == hit  # off by eight elements
+    assert c.ctx.rope(flat[:4096].view(2, 8, 4, 64), c.pos, out=flat[:4096].view(2, 4, 8, 64).transpose(1, 2), check=False) == hit
+    c.unchanged()
+    # rows beside one another in one buffer
+    c = Case(L=2)
+    wide = torch.zeros((2, 16, 12, 64), dtype=torch.bfloat16, device="cuda")
+    wide[:, :8, :4] = c.q
+    x = wide[:, :8, :4]
+    want = c.out.clone()
+    assert c.attend(out=want) == tri.TRI_OK
+    for other in (wide[:, :8, 4:8], wide[:, :8, 8:12], wide[:, 8:, :4], wide[:, 8:, 2:6]):
+        assert c.attend(q=x, out=other) == tri.TRI_OK
+        assert torch.equal(other, want) and torch.equal(x, c.q)
+    turned = c.ctx.rope(c.q, c.pos)
+    assert c.ctx.rope(x, c.pos, out=wide[:, 8:, 8:12], check=False) == tri.TRI_OK
+    assert torch.equal(wide[:, 8:, 8:12], turned)
+    assert c.ctx.rope(x, c.pos, out=x, check=False) == tri.TRI_OK and torch.equal(x, turned)
+    c.ctx.close()
