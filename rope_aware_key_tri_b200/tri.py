@@ -184,13 +184,17 @@ _SCALINGS = {"plain": TRI_ROPE_PLAIN, "linear": TRI_ROPE_LINEAR, "ntk": TRI_ROPE
              "smooth": TRI_ROPE_SMOOTH}
 
 
-def rope_frequencies(rotary_dim, base, scaling="plain", factor=1.0, original_length=0.0, low=1.0, high=32.0):
+def rope_frequencies(rotary_dim, base, scaling="plain", factor=1.0, original_length=0.0, low=1.0, high=None):
     """(omega fp64 [rotary_dim/2], magnitude) for :meth:`TriContext.rope_load`: "plain", "linear", "ntk", "yarn" or
-    "smooth" (or the TRI_ROPE_* value). Host only."""
+    "smooth" (or the TRI_ROPE_* value). low, high: the turns over original_length between which "yarn" and "smooth" go from
+    interpolated to unscaled (high=None: 32 for "yarn", 4 for "smooth", their usual values). Host only."""
+    kind = int(_SCALINGS.get(scaling, scaling))
+    if high is None:
+        high = 4.0 if kind == TRI_ROPE_SMOOTH else 32.0
     omega = np.empty(max(0, int(rotary_dim)) // 2, dtype=np.float64)
     mag = ctypes.c_double()
-    st = _lib.tri_rope_frequencies(int(rotary_dim), float(base), int(_SCALINGS.get(scaling, scaling)), float(factor),
-                                   float(original_length), float(low), float(high), omega.ctypes.data, ctypes.byref(mag))
+    st = _lib.tri_rope_frequencies(int(rotary_dim), float(base), kind, float(factor), float(original_length), float(low),
+                                   float(high), omega.ctypes.data, ctypes.byref(mag))
     if st != TRI_OK:
         raise TriError(st, "tri_rope_frequencies")
     return omega, mag.value

@@ -45,3 +45,12 @@ def test_fewer_pages_than_the_pools_hold():
     for L, n in ((2, 3), (1, 5), (2, 5)):
         with pytest.raises(ValueError, match="n_pages"):
             _append(ctx, L=L, n_pages=n)
+
+
+def test_default_turns_of_the_scaled_tables():
+    """"yarn" ramps up to 32 turns over the original length, "smooth" up to 4."""
+    for kind, high in (("yarn", 32.0), ("smooth", 4.0)):
+        for name in (kind, tri._SCALINGS[kind]):
+            got, mag = tri.rope_frequencies(64, 1e6, name, 8.0, 8192)
+            want, wmag = tri.rope_frequencies(64, 1e6, kind, 8.0, 8192, 1.0, high)
+            assert (got == want).all() and mag == wmag
