@@ -68,7 +68,7 @@ struct __align__(16) ChunkEntry {
     int s, tok0, ntok, len;   // sequence, first token (global row), tokens of the block, cached rows
     int first, kt0, kt1;      // keys seen by the block's first row, key tiles
     int pair;                 // one row tile whose key tiles the two warpgroups take in turn
-    int nsplit, split, slot, unused;  // splits of the block; this one; its first partial
+    int nsplit, split, slot;  // splits of the block; this one; its first partial
 };
 
 struct __align__(16) ChunkSeq {
@@ -273,7 +273,6 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
         x.nsplit = 1;
         x.split = 0;
         x.slot = 0;
-        x.unused = 0;
         x.pair = 0;
         return x;
     };
@@ -500,16 +499,6 @@ struct ChunkRing {
         }
     }
 };
-// A (bf16 pairs, one row per lane) in tensor memory.
-__device__ __forceinline__ void chunk_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, int acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 b, {%2, %5};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(acc), "r"(kDescHigh)
-        : "memory");
-}
 
 #define TRI_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
 #define TRI_U8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])

@@ -205,23 +205,20 @@ def tri_rope_load(ctx, rotary_dim: int, layout: int, omega, magnitude: float) ->
     return _lib.tri_rope_load(ctx, int(rotary_dim), int(layout), om.ctypes.data, float(magnitude))
 
 
+# (the prompt side's calls are short: structures and numbers are converted by the argtypes alone)
 def tri_rope(ctx, x: tri_rows, out: tri_rows, n_layers: int, n_tokens: int, n_heads: int, head_dim: int, pos_ptr: int,
              inverse: int, stream: int) -> int:
-    return _lib.tri_rope(ctx, ctypes.byref(x), ctypes.byref(out), int(n_layers), int(n_tokens), int(n_heads), int(head_dim),
-                         pos_ptr, int(inverse), stream)
+    return _lib.tri_rope(ctx, x, out, n_layers, n_tokens, n_heads, head_dim, pos_ptr, inverse, stream)
 
 
 def tri_append_chunk(ctx, kv: tri_kv, K_new: tri_rows, V_new: tri_rows, cu_ptr: int, pos_ptr: int, n_tokens: int,
                      rotate: int, q: Optional[tri_rows], q_out: Optional[tri_rows], stream: int) -> int:
-    return _lib.tri_append_chunk(ctx, ctypes.byref(kv), ctypes.byref(K_new), ctypes.byref(V_new), cu_ptr, pos_ptr,
-                                 int(n_tokens), int(rotate), None if q is None else ctypes.byref(q),
-                                 None if q_out is None else ctypes.byref(q_out), stream)
+    return _lib.tri_append_chunk(ctx, kv, K_new, V_new, cu_ptr, pos_ptr, n_tokens, rotate, q, q_out, stream)
 
 
 def tri_chunk_attention(ctx, kv: tri_kv, q: tri_rows, cu_ptr: int, n_tokens: int, scale: float, causal: int,
                         out: tri_rows, lse_ptr: Optional[int], stream: int) -> int:
-    return _lib.tri_chunk_attention(ctx, ctypes.byref(kv), ctypes.byref(q), cu_ptr, int(n_tokens), float(scale),
-                                    int(causal), ctypes.byref(out), lse_ptr, stream)
+    return _lib.tri_chunk_attention(ctx, kv, q, cu_ptr, n_tokens, scale, causal, out, lse_ptr, stream)
 
 
 def tri_get_error(ctx, stream: int):
@@ -514,8 +511,8 @@ class TriContext:
             raise ValueError(f"out must be shaped like x {tuple(x.shape)}, got {tuple(out.shape)}")
         rows, rout = make_rows(x, "x", self.device), make_rows(out, "out", self.device)
         T, H, d = x.shape[-3:]
-        st = _lib.tri_rope(self.handle, rows, rout, x.shape[0] if x.dim() == 4 else 1, T, H, d,
-                           self._flat("pos", pos, torch.int32, (T,)), bool(inverse), self._stream(stream))
+        st = tri_rope(self.handle, rows, rout, x.shape[0] if x.dim() == 4 else 1, T, H, d,
+                      self._flat("pos", pos, torch.int32, (T,)), bool(inverse), self._stream(stream))
         if not check:
             return st
         if st != TRI_OK:
@@ -549,9 +546,8 @@ class TriContext:
             q_out = q if q_out is None else q_out
             Hq = self._heads("q", q)
             qr, qo = self._tokens("q", q, L, T, Hq, d), self._tokens("q_out", q_out, L, T, Hq, d)
-        st = _lib.tri_append_chunk(self.handle, kv, kn, vn, self._flat("cu_new", cu_new, torch.int32, (B + 1,)),
-                                   self._flat("pos_new", pos_new, torch.int32, (T,)), T, bool(rotate), qr, qo,
-                                   self._stream(stream))
+        st = tri_append_chunk(self.handle, kv, kn, vn, self._flat("cu_new", cu_new, torch.int32, (B + 1,)),
+                              self._flat("pos_new", pos_new, torch.int32, (T,)), T, bool(rotate), qr, qo, self._stream(stream))
         if check and st != TRI_OK:
             raise TriError(st, "tri_append_chunk", tri_last_error(self.handle))
         return st
@@ -571,9 +567,9 @@ class TriContext:
         if lse is not None and (lse.dtype is not torch.float32 or lse.numel() != L * T * Hq or not lse.is_contiguous()
                                 or lse.get_device() != self.device):
             raise ValueError(f"lse must be a contiguous float32 tensor [{L}][{T}][{Hq}] on cuda:{self.device}")
-        st = _lib.tri_chunk_attention(self.handle, kv, qr, self._flat("cu_q", cu_q, torch.int32, (B + 1,)), T,
-                                      d ** -0.5 if scale is None else scale, bool(causal), ro,
-                                      None if lse is None else lse.data_ptr(), self._stream(stream))
+        st = tri_chunk_attention(self.handle, kv, qr, self._flat("cu_q", cu_q, torch.int32, (B + 1,)), T,
+                                 d ** -0.5 if scale is None else scale, bool(causal), ro,
+                                 None if lse is None else lse.data_ptr(), self._stream(stream))
         if not check:
             return st
         if st != TRI_OK:
