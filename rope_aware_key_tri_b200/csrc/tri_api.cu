@@ -1570,15 +1570,16 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
 
 // Turns per position of the bands, to the device (replaces the table before).
 tri_status set_rope_table(tri_ctx *c, const double *omega, int rotary_dim, int layout, double magnitude) {
-    std::vector<double> turns((size_t)rotary_dim / 2);
-    for (size_t f = 0; f < turns.size(); ++f) turns[f] = omega[f] / 6.283185307179586476925;
+    double turns[kMaxRopeDim / 2];
+    const size_t bands = (size_t)rotary_dim / 2;
+    for (size_t f = 0; f < bands; ++f) turns[f] = omega[f] / 6.283185307179586476925;
     const DeviceGuard guard(c->device);
     if (guard.error != cudaSuccess) return cuda_fail(c, guard.error, "cudaSetDevice");
     cudaError_t ce;
     // the synchronous copy follows work already launched on blocking streams; a table is otherwise
     // replaced only when no call uses it
     if ((ce = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(c, ce, "cudaDeviceSynchronize");
-    ce = cudaMemcpy(c->d_turns, turns.data(), sizeof(double) * turns.size(), cudaMemcpyHostToDevice);
+    ce = cudaMemcpy(c->d_turns, turns, sizeof(double) * bands, cudaMemcpyHostToDevice);
     if (ce != cudaSuccess) return cuda_fail(c, ce, "cudaMemcpy(rotary table)");
     c->rope_dim = rotary_dim;
     c->rope_layout = layout;
@@ -1722,10 +1723,10 @@ tri_status tri_calibrate_load(tri_ctx *c, int n_layers, int n_kv_heads, int grou
     c->G = group;
     c->D = D;
     c->layout = layout;
-    c->loaded = true;
     // until tri_rope_load, tokens are rotated at the statistics' own frequencies
-    if (!c->rope_loaded) return set_rope_table(c, omega.data(), D, layout, 1.0);
-    return TRI_OK;
+    const tri_status st = c->rope_loaded ? TRI_OK : set_rope_table(c, omega.data(), D, layout, 1.0);
+    c->loaded = st == TRI_OK;
+    return st;
 }
 
 tri_status tri_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double original_length,
