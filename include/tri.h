@@ -355,8 +355,8 @@ TRI_API tri_status tri_rope_load(tri_ctx *ctx, int rotary_dim, int layout, const
  *   pos      int32 [n_tokens] device: any int32 position
  *   inverse  0: rotate. Otherwise rotate back, divided by the magnitude: what post-RoPE rows were before
  *            (pre-RoPE queries for tri_calibrate_estimate, from cached or logged ones)
- * The angle is exact to about 2^-24 radians at every position, the products run in fp32, and the result is
- * rounded to bf16 once. One launch on `stream`. n_tokens 0 is accepted. Errors: TRI_EINVAL, TRI_ESTATE (no table),
+ * The angle is good to about 2^-23 radians plus 3 * 2^-53 |omega_f p| (measured: 2^-23.3 for positions up to 2^24, 2^-21.3
+ * at the ends of int32, for frequencies up to 1); the products run in fp32, and the result is rounded to bf16 once. One launch on `stream`. n_tokens 0 is accepted. Errors: TRI_EINVAL, TRI_ESTATE (no table),
  * TRI_EUNSUPPORTED, TRI_ECUDA.
  */
 TRI_API tri_status tri_rope(tri_ctx *ctx, const tri_rows *x, const tri_rows *out, int n_layers, int n_tokens,
@@ -403,7 +403,8 @@ TRI_API tri_status tri_append_chunk(tri_ctx *ctx, const tri_kv *kv, const tri_ro
  *           exp(logit), with which attentions over other rows can be joined
  * A query that sees no row (lens[s] of 0, or a query in front of the first row) gets zeros and an lse of -infinity. Rows
  * at or past lens[s] and rows that a query does not see may hold anything, NaN included. Logits, softmax statistics and
- * accumulators are fp32; the weights are rounded to bf16 for the tensor cores (2^-9 each), the result once more.
+ * accumulators are fp32; the weights are rounded to bf16 for the tensor cores (by at most 2^-8 each), the result once more.
+ * (Hidden values that are not finite cost the rows before them time: about 0.2 us for each key that such a row sees.)
  * Tokens outside every range are left unwritten; so are those of a refused sequence (TRI_DEV_LEN_GT_CAP,
  * TRI_DEV_BAD_PAGE; TRI_DEV_BAD_RANGE refuses all). A wait that ran out (TRI_DEV_TIMEOUT) leaves the result of
  * that call incomplete. Three launches on `stream` (a plan, the attention and the join of its parts, each a
@@ -457,8 +458,8 @@ TRI_API tri_status tri_get_failed_units(tri_ctx *ctx, void *stream, int32_t *uni
  *   unit        index (as in tri_get_error) of a unit whose first key copy the scoring kernels and
  *               tri_chunk_attention arm but never issue on the next calls, so that the wait for it runs
  *               out; -1 = off
- *   wait_tries  tries of the bounded waits, about 1 ms each (0 = the default 1024); the fused
- *               CUDA-core kernel's key-stream wait keeps the default bound (about one second)
+ *   wait_tries  tries of the bounded waits, about 8 us each on a B200 (0 = the default 1024); the fused
+ *               CUDA-core kernel's key-stream wait keeps the default bound (about 8 ms)
  * The withheld copy never lands, the wait gives up after wait_tries tries, the kernel records
  * TRI_DEV_TIMEOUT and leaves the affected units uncompacted (unit-level failure); no copy is
  * left in flight and nothing waits without bound.

@@ -113,7 +113,7 @@ struct MxArgs {
     unsigned long long *status;
     long long unit_base;         // added to the unit index in device status reports
     const int32_t *seq_bad;      // [batch] sequences refused by the validation kernel (no tiles)
-    int wait_tries;              // tries (about 1 ms each) of every bounded wait
+    int wait_tries;              // tries (about 8 us each) of every bounded wait
     long long inject_unit;       // test hook: the unit whose first key tile is withheld (-1: none)
     unsigned *unit_next;         // the fused kernel's unit counter, zeroed here for the launch after
 };
