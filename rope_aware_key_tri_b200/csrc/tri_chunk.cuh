@@ -603,7 +603,7 @@ __device__ __forceinline__ void chunk_lane(const typename ChunkLane<E>::Vec &w, 
 // met a NaN. What is not finite for a reason that the row does see stays as it is; telling so costs a look at the item's
 // hidden values (at most 383 keys). `in_block`: the row among the block's, `slot` where the item's part lies.
 // Its code is kept small, for calls that never run it pay for its size: 1 us here (of the 40 for 16 single tokens), 5 us
-// when the merge kernel held it.
+// when the merge kernel held it in a faster form.
 template <int D>
 __device__ __forceinline__ void chunk_row_again(const ChunkArgs &a, const ChunkEntry &en, int lr, int g, long long slot, int in_block) {
     constexpr int E = D / 32;  // lane's dims: [lane * E, + E)
@@ -684,6 +684,11 @@ __device__ __forceinline__ void chunk_row_again(const ChunkArgs &a, const ChunkE
 __device__ __forceinline__ unsigned chunk_item(int r) {
     const int pos = (r & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
     return (unsigned)r * gridDim.x + (unsigned)pos;
+}
+
+// (Not inline: inlined in the five places that call it, it cost every call 1 us by its size.)
+__device__ __noinline__ void chunk_timed_out(unsigned long long *status, int n_kv, int batch, int s, int lh) {
+    record_status(status, kDevTimeout, ((long long)(lh / n_kv) * batch + s) * n_kv + lh % n_kv);
 }
 
 // A 128-key tile of one row: S from tensor memory, masked, into the running (m, l); P over S. `left`: the
@@ -865,7 +870,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int G = a.group, LH = a.n_layers * a.n_kv;
     const unsigned n_items = (unsigned)a.head->n_entries * (unsigned)LH;  // below 2^31
     auto fail = [&](const ChunkEntry &e, int lh) {
-        record_status(a.status, kDevTimeout, ((long long)(lh / a.n_kv) * a.batch + e.s) * a.n_kv + lh % a.n_kv);
+        chunk_timed_out(a.status, a.n_kv, a.batch, e.s, lh);
         *abort_flag = 1;
     };
 
