@@ -72,12 +72,12 @@ struct tri_ctx {
         size_t bytes = 0;
     } ws_new_len, ws_plan, ws_part;
     std::vector<void *> ws_old;
-    // CTAs done of tri_append_chunk and of the attention's plan, zero between calls. Not part of the blocks above, which a
-    // call may replace and then fail.
+    // CTAs done of tri_append_chunk, zero between calls. Not part of the blocks above, which a call may replace and then
+    // fail; nor is that of the attention's plan, behind the status word.
     unsigned *d_ticket = nullptr;
     bool chunk_ready[2] = {false, false};  // the attention kernels' shared memory has been opted in to
     // device bookkeeping
-    unsigned long long *d_status = nullptr;
+    unsigned long long *d_status = nullptr;  // [0] the status word, [1] the attention's plan CTAs done
     // [0] CTAs of the fused kernel done, [1] its next free unit
     unsigned int *d_counter = nullptr;
     int32_t *d_seq_bad = nullptr;    // per-sequence verdict of the validation kernel
@@ -1507,7 +1507,6 @@ tri_status run_chunk_attention(tri_ctx *c, const tri_kv *kv, const tri_rows *q, 
     if ((st = ensure_block(c, &c->ws_part, (part_floats + ml_floats) * sizeof(float), "cudaMalloc(attention parts)")) != TRI_OK)
         return st;
     unsigned char *ws = static_cast<unsigned char *>(c->ws_plan.p);
-    a.ticket = c->d_ticket + 1;
     a.head = reinterpret_cast<tri::ChunkHead *>(ws + o_head);
     a.seqs = reinterpret_cast<tri::ChunkSeq *>(ws + o_seqs);
     a.base = reinterpret_cast<int *>(ws + o_base);
@@ -1609,18 +1608,18 @@ tri_status tri_create(tri_ctx **out, int device) {
     c->device = device;
     c->sm_count = p.multiProcessorCount;
     c->max_smem_optin = (int)p.sharedMemPerBlockOptin;
-    if (cudaMalloc(&c->d_status, sizeof(unsigned long long)) != cudaSuccess ||
+    if (cudaMalloc(&c->d_status, 2 * sizeof(unsigned long long)) != cudaSuccess ||
         cudaMalloc(&c->d_counter, 2 * sizeof(unsigned int)) != cudaSuccess ||
         cudaMalloc(&c->d_turns, sizeof(double) * kMaxRopeDim / 2) != cudaSuccess ||
-        cudaMalloc(&c->d_ticket, 2 * sizeof(unsigned)) != cudaSuccess ||
+        cudaMalloc(&c->d_ticket, sizeof(unsigned)) != cudaSuccess ||
         cudaMalloc(&c->d_fail_count, sizeof(unsigned)) != cudaSuccess ||
         cudaMalloc(&c->d_fail_units, sizeof(int32_t) * kFailCap) != cudaSuccess) {
         tri_destroy(c);
         return TRI_ENOMEM;
     }
-    if (cudaMemset(c->d_status, 0, sizeof(unsigned long long)) != cudaSuccess ||
+    if (cudaMemset(c->d_status, 0, 2 * sizeof(unsigned long long)) != cudaSuccess ||
         cudaMemset(c->d_counter, 0, 2 * sizeof(unsigned int)) != cudaSuccess ||
-        cudaMemset(c->d_ticket, 0, 2 * sizeof(unsigned)) != cudaSuccess ||
+        cudaMemset(c->d_ticket, 0, sizeof(unsigned)) != cudaSuccess ||
         cudaMemset(c->d_fail_count, 0, sizeof(unsigned)) != cudaSuccess) {
         tri_destroy(c);
         return TRI_ECUDA;

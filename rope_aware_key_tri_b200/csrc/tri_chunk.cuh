@@ -98,7 +98,6 @@ struct ChunkArgs {
     long long o_l, o_t, o_h;
     float *lse;               // [n_layers][n_tokens][Hq] or null
     const uint16_t *K, *V;
-    unsigned *ticket;         // plan CTAs done (the context's; back to 0 at the end)
     // workspace
     ChunkHead *head;
     ChunkSeq *seqs;           // [batch]
@@ -108,6 +107,8 @@ struct ChunkArgs {
     float *part;              // [slot][tile][D / 4][128][4], then [slot][tile][128][2] (m, l)
     float *part_ml;
     ChunkEntry *merges;       // the blocks that are split
+    // the context's status word, and behind it the count of the plan's CTAs that are done, back to 0 at the end. (A pointer of
+    // its own, 8 bytes more of arguments, cost 1.3 us of host time in every call.)
     unsigned long long *status;
     int wait_tries;
     long long inject_unit;
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
             a.seqs[s0] = ChunkSeq{lo, hi - lo, len, bad};
             if (bad) record_status(a.status, bad, (long long)s0 * a.n_kv);
             __threadfence();
-            sh_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+            sh_last = atomicAdd(reinterpret_cast<unsigned *>(a.status + 1), 1u) == gridDim.x - 1;
         }
     }
     if (!alone) {
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(kChunkPlanThreads) tri_chunk_plan_kernel(const
         sh_run = 0;
         sh_sum = 0;
         sh_max = 0;
-        if (!alone) *a.ticket = 0;
+        if (!alone) *reinterpret_cast<unsigned *>(a.status + 1) = 0;
     }
     __syncthreads();
     const int G = a.group, tpb = kChunkRows / G;
