@@ -57,3 +57,60 @@ def test_values(group, page, new, lens, d, aim):
 def test_values_of_layers_without_a_mask(d):
     _run(91, 3, 2, 2, d, 32, [40, 3, 129], [1000, 2500, 600], causal=False, aim=True)
     _run(92, 2, 8, 1, d, 80, [256], [4096], causal=False)
+
+
+def test_sequences_that_share_pages():
+    """A common prefix held once: the same page ids in several rows of the block table, one of them twice in a row."""
+    g = torch.Generator().manual_seed(95)
+    d, group, page, lens = 128, 4, 16, [500, 330, 64]
+    ctx = pu.context(1, 2, group, d)
+    pool = pu.Paged(g, 1, 2, d, page, lens)
+    t = pool.table_host
+    t[1, :12] = t[0, :12]
+    t[2, :4] = [t[0, 3], t[0, 3], t[1, 20], t[0, 0]]
+    pool.table = torch.from_numpy(t).cuda()
+    new = [30, 1, 64]
+    q = pu.bf16(g, (1, sum(new), 2 * group, d), 2.0)
+    c = np.concatenate([[0], np.cumsum(new)])
+    out = ctx.chunk_attention(pool.K, pool.V, torch.tensor(lens, dtype=torch.int32).cuda(), q,
+                              torch.tensor(c, dtype=torch.int32).cuda(), block_table=pool.table)
+    assert ctx.get_error()[0] == tri.TRI_OK
+    for b, (n, m) in enumerate(zip(new, lens)):
+        k, v = pool.rows(pool.K, b, m)[0], pool.rows(pool.V, b, m)[0]
+        for h in range(2 * group):
+            rows = q[0, c[b]:c[b + 1], h]
+            p = ac.weights(rows, k[h // group], m - n + 1, d ** -0.5)
+            assert ac.excess(out[0, c[b]:c[b + 1], h], p, rows, k[h // group], v[h // group], d ** -0.5) <= 1.0
+    ctx.close()
+
+
+def test_rows_past_32_bits():
+    """Pages whose elements lie beyond the 2^31st (4.3 GB each of keys and values): appended, attended, and a value that is not
+    finite hidden from some queries, which are then computed row by row."""
+    g = torch.Generator().manual_seed(96)
+    d, group, page, n, m = 64, 4, 64, 40, 200
+    pages = (1 << 31) // (page * d) + 8
+    ctx = pu.context(1, 1, group, d)
+    K = torch.empty((1, pages, 1, page, d), dtype=torch.bfloat16, device="cuda")
+    V = torch.empty_like(K)
+    P = torch.empty((1, pages, 1, page), dtype=torch.int32, device="cuda")
+    ids = torch.tensor([pages - 1, 3, pages - 5, pages - 2], dtype=torch.int32)
+    table, at = ids[None].cuda(), ids.long().cuda()
+    k, v = pu.bf16(g, (1, m, 1, d), 0.6), pu.bf16(g, (1, m, 1, d))
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ctx.append_chunk(K, V, P, lens, k, v, torch.tensor([0, m], dtype=torch.int32).cuda(), torch.arange(m, dtype=torch.int32).cuda(),
+                     block_table=table, rotate=False)
+    assert ctx.get_error()[0] == tri.TRI_OK and lens.item() == m
+    assert torch.equal(K[0, at, 0].reshape(-1, d)[:m], k[0, :, 0]) and torch.equal(V[0, at, 0].reshape(-1, d)[:m], v[0, :, 0])
+    assert torch.equal(P[0, at, 0].reshape(-1)[:m], torch.arange(m, dtype=torch.int32, device="cuda"))
+    q = pu.bf16(g, (1, n, group, d), 2.0)
+    hidden = m - n + 25
+    V[0, at[hidden // page], 0, hidden % page] = float("inf")
+    out = ctx.chunk_attention(K, V, lens, q, torch.tensor([0, n], dtype=torch.int32).cuda(), block_table=table)
+    assert ctx.get_error()[0] == tri.TRI_OK
+    for h in range(group):
+        rows = q[0, :25, h]
+        p = ac.weights(rows, k[0, :hidden, 0], m - n + 1, d ** -0.5)
+        assert ac.excess(out[0, :25, h], p, rows, k[0, :hidden, 0], v[0, :hidden, 0], d ** -0.5) <= 1.0
+    assert (~torch.isfinite(out[0, 25:])).all()
+    ctx.close()
