@@ -340,7 +340,8 @@ TRI_API tri_status tri_rope_frequencies(int rotary_dim, double base, int scaling
  * multiplied, as the complex number of its two dims, by magnitude e^{i omega_f p}. Dims at r and beyond stay.
  *   rotary_dim r  a multiple of 16, up to 128 and, in each call, up to the head_dim
  *   layout    TRI_ROPE_HALF: dims (f, f + r/2); TRI_ROPE_INTERLEAVED: dims (2f, 2f + 1)
- *   omega     host fp64 [r/2], finite, copied; magnitude > 0
+ *   omega     host fp64 [r/2], copied; finite, times 2^31 too
+ *   magnitude from 2^-126 to 2^126
  * Until this is called, the table is the loaded statistics' (base^(-2f/d) over the whole head, their layout).
  * It replaces the table for tri_rope and tri_append_chunk only: the scores of tri_prune keep the frequencies of
  * tri_calibrate_load. Synchronous (it waits for the device); a captured graph rotates by the table loaded
@@ -373,7 +374,8 @@ TRI_API tri_status tri_rope(tri_ctx *ctx, const tri_rows *x, const tri_rows *out
  *   pos_new   int32 [n_tokens] device: each token's position
  *   rotate    0: K_new is post-RoPE and copied. Otherwise keys are rotated at pos_new
  *   q, q_out  both NULL, or (with rotate) tri_rows [n_layers][n_tokens][n_kv_heads * group]: the tokens' queries are
- *             rotated in the same launch; q_out may be q itself, else they must not overlap
+ *             rotated in the same launch; q_out may be q itself, else they must not overlap. It must not overlap K_new
+ *             or V_new either
  * Token i of sequence s goes to slot lens[s] + i of each of its units, and lens_out[s] = lens[s] + its tokens. Pages
  * of those slots must be allocated; no page may be shared between the runs of two sequences. A sequence that
  * would pass its capacity or lacks a page is refused as a whole: nothing of it is written (no row, no query,

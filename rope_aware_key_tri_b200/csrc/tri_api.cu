@@ -1770,9 +1770,11 @@ tri_status tri_rope_load(tri_ctx *c, int rotary_dim, int layout, const double *o
     c->last_error[0] = 0;
     if (rotary_dim < 16 || rotary_dim % 16 != 0 || rotary_dim > kMaxRopeDim) return TRI_EINVAL;
     if (layout != TRI_ROPE_HALF && layout != TRI_ROPE_INTERLEAVED) return TRI_EINVAL;
-    if (!(magnitude > 0.0) || !std::isfinite(magnitude)) return TRI_EINVAL;
+    // the kernel multiplies by the magnitude and by its inverse in fp32, and by positions in fp64
+    constexpr double lo = std::numeric_limits<float>::min();
+    if (!(magnitude >= lo) || !(magnitude <= 1.0 / lo)) return TRI_EINVAL;
     for (int f = 0; f < rotary_dim / 2; ++f)
-        if (!std::isfinite(omega[f])) return TRI_EINVAL;
+        if (!std::isfinite(omega[f] * 2147483648.0)) return TRI_EINVAL;
     const tri_status st = set_rope_table(c, omega, rotary_dim, layout, magnitude);
     if (st == TRI_OK) c->rope_loaded = true;
     return st;

@@ -117,3 +117,24 @@ def test_outputs_that_lie_on_their_inputs():
     assert torch.equal(wide[:, 8:, 8:12], turned)
     assert c.ctx.rope(x, c.pos, out=x, check=False) == tri.TRI_OK and torch.equal(x, turned)
     c.ctx.close()
+
+
+def test_rotary_tables_that_the_arithmetic_does_not_hold():
+    """Magnitudes that are nothing or infinite in fp32, either way round, and frequencies whose angle is: refused, and the table
+    before them stays."""
+    c = Case()
+    omega, _ = tri.rope_frequencies(64, 1e4)
+    c.ctx.rope_load(omega, pu.HALF, 2.0 ** 126)
+    c.ctx.rope_load(omega, pu.HALF, 2.0 ** -126)
+    c.ctx.rope_load(omega, pu.HALF, 2.0)
+    for magnitude in (1e-300, 2.0 ** -127, 2.0 ** 127, 1e300, math.inf, math.nan, 0.0, -1.0):
+        with pytest.raises(tri.TriError) as e:
+            c.ctx.rope_load(omega, pu.HALF, magnitude)
+        assert e.value.status == tri.TRI_EINVAL
+    for w in (1e300, -1e308, math.inf):
+        with pytest.raises(tri.TriError):
+            c.ctx.rope_load(omega + w, pu.HALF)
+    # position 0: the magnitude alone
+    assert torch.equal(c.ctx.rope(c.q, torch.zeros_like(c.pos)), c.q * 2)
+    assert torch.equal(c.ctx.rope(c.q, torch.zeros_like(c.pos), inverse=True), c.q / 2)
+    c.unchanged()
