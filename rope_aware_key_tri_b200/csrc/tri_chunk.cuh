@@ -35,11 +35,11 @@
 // the unrounded weights. Weights in two bf16 parts would double the MMAs of P V.
 //
 // Bound, measured on a B200 with everything but one part of the kernel taken out (512 tokens of 64 heads over 32768
-// rows of 128 dims: 128 items of 256 tiles on 148 SMs; 510 us): the loads alone 343 us, the MMAs with their barriers 426 us,
+// rows of 128 dims: 128 items of 256 tiles on 148 SMs; 510 to 514 us): the loads alone 343 us, the MMAs with their barriers 426 us,
 // the rest is the chain of a tile from S through the exponentials (1100 clocks) to P V and the next S, whose barriers cost
 // about 300 clocks each way. 64-key steps with two S buffers take that chain apart, but an MMA of 64 keys takes
 // as long as one of 128, and the MMAs alone then took 3100 of 3900 clocks a tile: the same time. Few rows: the HBM (16 single
-// tokens over 2176 rows stream at 7 TB/s for 19 of 37 us; the rest is the plan, the first tiles' latency and the end).
+// tokens over 2176 rows stream at 7 TB/s for 19 of 38 us; the rest is the plan, the first tiles' latency and the end).
 #pragma once
 
 #include <cuda.h>
