@@ -621,7 +621,8 @@ __device__ __forceinline__ void chunk_row_again(const ChunkArgs &a, const ChunkE
     Vec *out = reinterpret_cast<Vec *>(a.out + lr * a.o_l + tok * a.o_t + head * a.o_h + lane * E);
     Acc *acc_out = reinterpret_cast<Acc *>(a.part + ((slot * (D / 4) + lane * E / 4) * 128 + (in_block & 127)) * 4 + lane * E % 4);
     unsigned todo = 0, hidden = 0;  // this lane's dims that are not finite here, and in a hidden value
-    float was[E], qv[E], acc[E], m = NEG_INF, l = 0.f;
+    alignas(16) float was[E];
+    float qv[E], acc[E], m = NEG_INF, l = 0.f;
     if (part) *reinterpret_cast<Acc *>(was) = *acc_out; else chunk_lane<E>(*out, was);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -673,7 +674,7 @@ __device__ __forceinline__ void chunk_row_again(const ChunkArgs &a, const ChunkE
     }
     // a part goes by the maximum that it was written with; one that sees no key weighs nothing, whatever it holds
     const float scale = l == 0.f ? 0.f : part ? ex2_approx(m - a.part_ml[(slot * 128 + (in_block & 127)) * 2]) : 1.f / l;
-    unsigned w[E / 2];
+    alignas(8) unsigned w[E / 2];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         if (todo >> e & 1u) was[e] = acc[e] * scale;

@@ -1,7 +1,9 @@
 """What the torch-facing calls of the prompt side check before the library sees a pointer, without a GPU: tensors on the CPU are taken
 for the context's device, and the library is handed no context, which it refuses (TRI_EINVAL) once every check has passed."""
+import math
 import types
 
+import numpy as np
 import pytest
 import torch
 
@@ -54,3 +56,19 @@ def test_default_turns_of_the_scaled_tables():
             got, mag = tri.rope_frequencies(64, 1e6, name, 8.0, 8192)
             want, wmag = tri.rope_frequencies(64, 1e6, kind, 8.0, 8192, 1.0, high)
             assert (got == want).all() and mag == wmag
+
+
+@pytest.mark.parametrize("r,base,factor,length,low,high", [(128, 1e6, 4.0, 8192, 1.0, 32.0), (64, 1e4, 8.0, 4096, 1.0, 32.0),
+                                                           (96, 5e5, 2.0, 32768, 0.5, 16.0), (16, 1e4, 40.0, 2048, 1.0, 32.0)])
+def test_yarn_ramp(r, base, factor, length, low, high):
+    """Every band: omega / factor and omega mixed by a ramp over the band index, from the last band that turns at least `high`
+    times over the length to the first that turns at most `low` times (as real indices, rounded outwards)."""
+    f = np.arange(r // 2)
+    omega = base ** (-2.0 * f / r)
+    index = lambda turns: r * math.log(length / (2 * math.pi * turns)) / (2 * math.log(base))
+    first, last = max(math.floor(index(high)), 0), min(math.ceil(index(low)), r - 1)
+    assert last > first
+    mix = np.clip((f - first) / (last - first), 0.0, 1.0)
+    got, magnitude = tri.rope_frequencies(r, base, "yarn", factor, length, low, high)
+    np.testing.assert_allclose(got, omega / factor * mix + omega * (1 - mix), rtol=1e-12)
+    assert math.isclose(magnitude, 1 + 0.1 * math.log(factor), rel_tol=1e-14)
