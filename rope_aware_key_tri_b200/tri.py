@@ -269,6 +269,14 @@ def _stream_handle(stream) -> int:
     return stream.cuda_stream
 
 
+def _new(shape, dtype, device, stream):
+    """A result's memory, of the stream that writes it: what the current stream freed may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _check_t(t, lens):
     if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.shape != lens.shape:
         raise ValueError(f"t must be a contiguous CUDA int32 tensor shaped like lens {tuple(lens.shape)}")
@@ -448,7 +456,7 @@ class TriContext:
                                 or not out.is_contiguous()):
             raise ValueError("out must be a contiguous float32 tensor shaped like q")
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+            out = _new(q.shape, torch.float32, q.device, stream)
         st = tri_decode_attention(self.handle, kv, q.data_ptr(), out.data_ptr(), _stream_handle(stream))
         if not check:
             return st
@@ -506,7 +514,7 @@ class TriContext:
         """Rotate the rows x (bf16 [tokens][heads][d] or [layers][tokens][heads][d], see make_rows) at pos (int32 [tokens]);
         inverse=True rotates back. Returns out (x itself is accepted), or the status when check is False."""
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            out = _new(x.shape, x.dtype, x.device, stream)
         if out.shape != x.shape:
             raise ValueError(f"out must be shaped like x {tuple(x.shape)}, got {tuple(out.shape)}")
         rows, rout = make_rows(x, "x", self.device), make_rows(out, "out", self.device)
@@ -561,7 +569,7 @@ class TriContext:
         kv, L, H, d, B = self._cache(K, V, None, lens, None, block_table, n_pages, layer_begin)
         T = q.shape[-3]
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = _new(q.shape, q.dtype, q.device, stream)
         Hq = self._heads("q", q)
         qr, ro = self._tokens("q", q, L, T, Hq, d), self._tokens("out", out, L, T, Hq, d)
         if lse is not None and (lse.dtype is not torch.float32 or lse.numel() != L * T * Hq or not lse.is_contiguous()
@@ -584,9 +592,7 @@ class TriContext:
             raise TriError(TRI_EINVAL, "tri_calibrate_estimate", "Q must be a contiguous bf16 [L][T][Hq][d] tensor")
         nl, T, Hq, d = Q.shape
         if out is None:
-            out = (torch.empty((nl, Hq, d), dtype=torch.float32, device=Q.device),
-                   torch.empty((nl, Hq, d // 2), dtype=torch.float32, device=Q.device),
-                   torch.empty((nl, Hq, d // 2), dtype=torch.float32, device=Q.device))
+            out = tuple(_new((nl, Hq, n), torch.float32, Q.device, stream) for n in (d, d // 2, d // 2))
         qm, qn, R = out
         st = tri_calibrate_estimate(self.handle, Q.data_ptr(), nl, T, Hq, d, int(layout), qm.data_ptr(),
                                     qn.data_ptr(), R.data_ptr(), _stream_handle(stream))
